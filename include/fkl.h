@@ -361,6 +361,144 @@ fkl_status fkl_topk(const fkl_topk_shape* shape, const void* h, const void* W,
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The 8-bit head: answering with a distilled (or teacher) head needs the same
+ * output projection as the loss, without its gradient. fkl_quantize holds a
+ * matrix in 8-bit integers with one scale for each row, and fkl_project
+ * multiplies token rows with such a matrix.
+ */
+typedef enum {
+  FKL_F32 = 0,
+  FKL_BF16 = 1,
+  FKL_F16 = 2,
+  FKL_I8 = 3
+} fkl_type;
+
+/*
+ * Rows in 8-bit integers. For every row r of x [rows, cols] (type FKL_F32,
+ * FKL_BF16 or FKL_F16; row stride ldx elements), with a = max_j |x[r,j]|:
+ *   scale[r] = a / 127                       (fp32, rounded to nearest)
+ *   q[r,j]   = 127 x[r,j] / a rounded to the nearest integer, ties to even;
+ *              the quotient is that of the real numbers, not of its rounding
+ * so x[r,j] is about scale[r] q[r,j], off by at most scale[r] / 2. A row of
+ * zeros gets scale 0 and zeros; a row that holds an infinity or a NaN gets
+ * scale NaN and zeros, so every product with it is NaN.
+ * q: int8, row stride ldq bytes; the bytes of a row past cols are not
+ * written. scale: fp32 [rows]. q must not overlap x. fkl_project reads q
+ * fastest where q and ldq are multiples of 16.
+ * Needs no workspace, and the debug build does not check it. rows may be 0.
+ * Errors: FKL_EINVAL (rows < 0, cols < 1, a stride below cols, NULL or
+ * misaligned arrays, another type), FKL_EUNSUPPORTED (rows or cols beyond
+ * 2^31 - 1025, a stride beyond 2^40), FKL_EDEVICE.
+ */
+fkl_status fkl_quantize(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
+                        float* scale, void* stream);
+
+/*
+ * Output projection (any linear layer's product) in 8-bit integers:
+ *   out[m,n] = a_scale[m] b_scale[n] sum_k a[m,k] b[n,k] + bias[n]
+ * a [M,K]: FKL_I8 rows with a_scale fp32 [M], or floating rows (FKL_F32,
+ * FKL_BF16, FKL_F16; a_scale NULL), which the call quantises first exactly as
+ * fkl_quantize does. b int8 [N,K] with b_scale fp32 [N]; bias fp32 [N] or
+ * NULL. out [M,N] of out_type FKL_F32, FKL_BF16 or FKL_F16. Row strides lda,
+ * ldb, ldo in elements.
+ * The sum is exact (32-bit integers; all of -128..127 is allowed), the scales
+ * and the bias are applied in fp32, and the result is rounded once.
+ * Any size and stride is accepted. An 8-bit operand whose row stride is a
+ * multiple of 16 (and at most 2^22) must be 16-byte aligned; it is read where
+ * it is, in whole 16-byte pieces: the bytes from a row's K to the next
+ * multiple of 16 are read too (their values do not matter), so the array must
+ * hold them in its last row as well. An operand with any other stride, or one
+ * that shape->flags names, is first copied to such rows in the workspace,
+ * wherever it starts.
+ * M may be 0. out must not overlap the inputs; elements of out past a row's N
+ * are not written.
+ * Errors: FKL_EINVAL (bad shape, type or flags, NULL or misaligned arrays,
+ * a_scale given with floating rows or missing with 8-bit ones), FKL_EUNSUPPORTED (K
+ * above 131071, where a 32-bit sum could overflow; M or N beyond
+ * 2^31 - 1025; a stride beyond 2^40), FKL_EWORKSPACE, FKL_EDEVICE.
+ * Deterministic.
+ */
+typedef struct {
+  int64_t M, N, K;        /* M >= 0, N >= 1, 1 <= K <= 131071 */
+  int64_t lda, ldb, ldo;  /* row strides in elements */
+  int32_t a_type;         /* FKL_I8, FKL_F32, FKL_BF16 or FKL_F16 */
+  int32_t out_type;       /* FKL_F32, FKL_BF16 or FKL_F16 */
+  uint32_t flags;         /* FKL_PROJECT_* below; 0 = default */
+} fkl_project_shape;
+
+#define FKL_PROJECT_COPY_A 0x1u /* copy 8-bit a to aligned rows first whatever its stride */
+#define FKL_PROJECT_COPY_B 0x2u /* the same for b */
+
+/*
+ * Workspace bytes of fkl_project for this shape (host only; bytes may be
+ * NULL): room for quantised rows of a and for copies of operands that are not
+ * read where they are.
+ * Errors: those of fkl_project that the shape alone decides.
+ */
+fkl_status fkl_project_workspace_size(const fkl_project_shape* shape, size_t* bytes);
+
+fkl_status fkl_project(const fkl_project_shape* shape, const void* a, const float* a_scale, const int8_t* b,
+                       const float* b_scale, const float* bias, void* out, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Sampling: one entry of each row of logits [N,V], drawn with temperature,
+ * top-k, top-p and min-p from a given random number u[r] in [0, 1).
+ *   masked entries: -inf and NaN. m = the row's largest logit (+inf allowed).
+ *   w[v] = exp((x[v] - m) / T): 1 where x[v] = m, 0 where masked.
+ *   The entries' order: larger logits first, equal ones by their position.
+ *   A    = the first top_k entries in that order (top_k <= 0 or >= V: all)
+ *   kept = the entries of A before which A's entries sum to less than
+ *          top_p * sum_A w (top_p >= 1 or NaN: all), and whose w >= min_p
+ *          (min_p <= 0 or NaN: all); the first entry is always kept
+ *   token   = the first position v, in the row's own order of positions, at
+ *             which the kept entries up to v sum to more than
+ *             u * sum_kept w (u < 0 or NaN is taken as 0, u >= 1 as just
+ *             below 1)
+ *   logprob = log(w[token] / sum_kept w)
+ * T = 0 is greedy: the largest logit, the lowest position among equals, with
+ * logprob 0. A row without unmasked entries, or whose per-row temperature is
+ * negative or not finite, gets token -1 and logprob -inf.
+ * The weights and their sums are held in 64 bits, so that the draw depends
+ * only on the inputs.
+ * logits: type FKL_F32, FKL_BF16 or FKL_F16, row stride ld elements. ids int32
+ * [N,V] (row stride ld_ids) or NULL: token then is ids[r, v] instead of the
+ * position v, as with a teacher cache's lists (fkl_topk). u fp32 [N]; token
+ * int32 [N]; logprob fp32 [N] or NULL. N may be 0.
+ * Errors: FKL_EINVAL (bad shape or type, NULL or misaligned arrays, a shared
+ * temperature that is negative or not finite, a shared top_p or min_p that is
+ * NaN), FKL_EUNSUPPORTED (N or V beyond 2^31 - 1025, a stride beyond 2^40),
+ * FKL_EWORKSPACE, FKL_EDEVICE. Deterministic.
+ */
+typedef struct {
+  int64_t N, V;    /* N >= 0 rows of V >= 1 logits */
+  int64_t ld;      /* row stride of the logits, elements */
+  int64_t ld_ids;  /* row stride of ids, elements; ignored without ids */
+  int32_t type;    /* FKL_F32, FKL_BF16 or FKL_F16 */
+} fkl_sample_shape;
+
+/* Each setting comes for every row (device array [N]) or, where that pointer
+ * is NULL, as one shared value. */
+typedef struct {
+  const float* temperature_rows;
+  const int32_t* top_k_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+  float temperature;
+  int32_t top_k;
+  float top_p;
+  float min_p;
+} fkl_sample_params;
+
+/* Workspace bytes of fkl_sample for this shape (host only; bytes may be
+ * NULL). Errors: those of fkl_sample that the shape alone decides. */
+fkl_status fkl_sample_workspace_size(const fkl_sample_shape* shape, size_t* bytes);
+
+fkl_status fkl_sample(const fkl_sample_shape* shape, const fkl_sample_params* params, const void* logits,
+                      const int32_t* ids, const float* u, int32_t* token, float* logprob, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * Kernel timing. While enabled (a process-wide switch), every launch of the
  * path's main kernels is bracketed by a pair of hipEvents recorded on the
  * call's own stream, tagged with the kernel name and the launch's

@@ -42,6 +42,14 @@ __all__ = [
     "TopkShape",
     "topk_workspace_size",
     "topk",
+    "quantize",
+    "ProjectShape",
+    "project_workspace_size",
+    "project",
+    "SampleShape",
+    "SampleParams",
+    "sample_workspace_size",
+    "sample",
     "trace_enable",
     "trace_read",
     "EXPORTED_SYMBOLS",
@@ -61,6 +69,11 @@ EXPORTED_SYMBOLS = (
     "fkl_plan_info",
     "fkl_topk_workspace_size",
     "fkl_topk",
+    "fkl_quantize",
+    "fkl_project_workspace_size",
+    "fkl_project",
+    "fkl_sample_workspace_size",
+    "fkl_sample",
     "fkl_trace_enable",
     "fkl_trace_read",
     "fkl_status_string",
@@ -142,6 +155,49 @@ class TopkShape(ctypes.Structure):
     ]
 
 
+class ProjectShape(ctypes.Structure):
+    """Mirror of ``fkl_project_shape``."""
+
+    _fields_ = [
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("lda", ctypes.c_int64),
+        ("ldb", ctypes.c_int64),
+        ("ldo", ctypes.c_int64),
+        ("a_type", ctypes.c_int32),
+        ("out_type", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
+class SampleShape(ctypes.Structure):
+    """Mirror of ``fkl_sample_shape``."""
+
+    _fields_ = [
+        ("N", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("ld_ids", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+    ]
+
+
+class SampleParams(ctypes.Structure):
+    """Mirror of ``fkl_sample_params``."""
+
+    _fields_ = [
+        ("temperature_rows", ctypes.c_void_p),
+        ("top_k_rows", ctypes.c_void_p),
+        ("top_p_rows", ctypes.c_void_p),
+        ("min_p_rows", ctypes.c_void_p),
+        ("temperature", ctypes.c_float),
+        ("top_k", ctypes.c_int32),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+    ]
+
+
 TOPK_DIRECT = 0x1
 TOPK_MATERIALIZE = 0x2
 
@@ -171,11 +227,19 @@ def lib() -> ctypes.CDLL:
     tshp = ctypes.POINTER(TopkShape)
     L.fkl_topk_workspace_size.argtypes = [tshp, ctypes.POINTER(sz)]
     L.fkl_topk.argtypes = [tshp, vp, vp, vp, vp, vp, sz, vp]
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    pshp, sshp = ctypes.POINTER(ProjectShape), ctypes.POINTER(SampleShape)
+    L.fkl_quantize.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp]
+    L.fkl_project_workspace_size.argtypes = [pshp, ctypes.POINTER(sz)]
+    L.fkl_project.argtypes = [pshp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.fkl_sample_workspace_size.argtypes = [sshp, ctypes.POINTER(sz)]
+    L.fkl_sample.argtypes = [sshp, ctypes.POINTER(SampleParams), vp, vp, vp, vp, vp, vp, sz, vp]
     L.fkl_trace_enable.argtypes = [ctypes.c_int]
     L.fkl_trace_read.argtypes = [ctypes.POINTER(KernelStat), ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     for f in ("fkl_workspace_size", "fkl_forward", "fkl_forward_static", "fkl_backward", "fkl_validate_teacher", "fkl_validate_terms",
               "fkl_plan_info", "fkl_version",
-              "fkl_topk_workspace_size", "fkl_topk", "fkl_trace_enable", "fkl_trace_read"):
+              "fkl_topk_workspace_size", "fkl_topk", "fkl_quantize", "fkl_project_workspace_size", "fkl_project",
+              "fkl_sample_workspace_size", "fkl_sample", "fkl_trace_enable", "fkl_trace_read"):
         getattr(L, f).restype = ctypes.c_int
     L.fkl_status_string.argtypes = [ctypes.c_int]
     L.fkl_status_string.restype = ctypes.c_char_p
@@ -517,6 +581,190 @@ def topk(h, W, K: int, chunk: int = 0, workspace=None, t_idx=None, t_logit=None,
         _check(lib().fkl_topk(ctypes.byref(s), _ptr(h), _ptr(W), _ptr(t_idx), _ptr(t_logit), _ptr(ws),
                               ctypes.c_size_t(_nbytes(ws)), _stream(h.device)))
     return t_idx, t_logit
+
+
+# Element types (fkl_type in include/fkl.h).
+_F32, _BF16, _F16, _I8 = 0, 1, 2, 3
+_types = None
+
+
+def _type_of(t, name, integers=False):
+    """fkl_type of a tensor's elements."""
+    global _types
+    if _types is None:
+        torch = _torch()
+        _types = {torch.float32: _F32, torch.bfloat16: _BF16, torch.float16: _F16, torch.int8: _I8}
+    code = _types.get(t.dtype if hasattr(t, "dtype") else t)
+    if code is None or (code == _I8 and not integers):
+        raise TypeError(f"{name} must be float32, bfloat16 or float16{' or int8' if integers else ''}, "
+                        f"got {t.dtype if hasattr(t, 'dtype') else t}")
+    return code
+
+
+def _matrix(t, name, device=None):
+    """Checks a 2-D GPU tensor whose rows are contiguous; returns (rows, columns, row stride)."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}; got {t.device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:  # one row has no stride
+        ld = max(ld, cols)
+    elif ld < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return rows, cols, ld
+
+
+def quantize(x, q=None, scale=None):
+    """Rows in 8-bit integers with a scale each: scale = max |x| / 127, q = 127 x / max |x| rounded to
+    the nearest integer (ties to even), for every row of x [M, K] (float32, bfloat16 or float16, rows
+    contiguous). Returns (q int8 [M, K], scale fp32 [M]). q is allocated with rows padded to a multiple of
+    16 bytes, the layout that project() reads where it is (a view: q.stride(0) may exceed K)."""
+    torch = _torch()
+    M, K, ldx = _matrix(x, "x")
+    code = _type_of(x, "x")
+    if q is None:
+        q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)[:, :K]
+    if _matrix(q, "q", x.device)[:2] != (M, K) or q.dtype != torch.int8:
+        raise ValueError(f"q must be int8 with shape {(M, K)}, got {q.dtype} with {tuple(q.shape)}")
+    if scale is None:
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    _need(scale, "scale", torch.float32, (M,), x.device)
+    with _on(x.device):
+        _check(lib().fkl_quantize(M, K, code, x.data_ptr(), ldx, q.data_ptr(), max(q.stride(0), K), scale.data_ptr(),
+                                  _stream(x.device)))
+    return q, scale
+
+
+PROJECT_COPY_A = 0x1
+PROJECT_COPY_B = 0x2
+
+
+def _read_where_it_is(t, rows, cols, ld):
+    """Whether the library may read an int8 operand in place: 16-byte aligned, and its last row's
+    last 16-byte piece inside the tensor's storage."""
+    if ld % 16 or t.data_ptr() % 16:
+        return False
+    return rows == 0 or t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16 <= t.untyped_storage().nbytes()
+
+
+def project_workspace_size(M, N, K, a_dtype=None, out_dtype=None, lda=None, ldb=None, ldo=None, flags=0) -> int:
+    """Workspace bytes of project() for this shape (a_dtype int8 and contiguous rows unless given)."""
+    torch = _torch()
+    s = ProjectShape(M, N, K, K if lda is None else lda, K if ldb is None else ldb, N if ldo is None else ldo,
+                     _type_of(a_dtype or torch.int8, "a", True), _type_of(out_dtype or torch.bfloat16, "out"), flags)
+    b = ctypes.c_size_t(0)
+    _check(lib().fkl_project_workspace_size(ctypes.byref(s), ctypes.byref(b)))
+    return b.value
+
+
+def project(a, b, b_scale, a_scale=None, bias=None, out_dtype=None, out=None, workspace=None):
+    """Output projection (any linear layer's product) over 8-bit rows, fkl_project of include/fkl.h:
+    out[m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k] + bias[n], the sum exact in 32-bit integers,
+    the rest in fp32, rounded once to out_dtype (bfloat16 unless out or out_dtype says otherwise).
+
+    a: int8 [M, K] with a_scale fp32 [M], or float32 / bfloat16 / float16 [M, K] without, which is
+    quantised first as quantize() does. b: int8 [N, K] with b_scale fp32 [N], as quantize() returns them.
+    bias: fp32 [N]. Rows may be strided; int8 rows that are not 16-byte aligned are copied first. For
+    inference: no gradient flows through it."""
+    torch = _torch()
+    M, K, lda = _matrix(a, "a")
+    dev = a.device
+    N, Kb, ldb = _matrix(b, "b", dev)
+    if b.dtype != torch.int8:
+        raise TypeError(f"b must be int8, got {b.dtype}")
+    if Kb != K:
+        raise ValueError(f"a and b must have the same number of columns, got {K} and {Kb}")
+    code = _type_of(a, "a", True)
+    _need(b_scale, "b_scale", torch.float32, (N,), dev)
+    if (a_scale is None) != (code != _I8):
+        raise ValueError("a_scale goes with an int8 a; a floating a is quantised by the call")
+    if a_scale is not None:
+        _need(a_scale, "a_scale", torch.float32, (M,), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    if _matrix(out, "out", dev)[:2] != (M, N):
+        raise ValueError(f"out must have shape {(M, N)}, got {tuple(out.shape)}")
+    flags = 0
+    if code == _I8 and not _read_where_it_is(a, M, K, lda):
+        flags |= PROJECT_COPY_A
+    if not _read_where_it_is(b, N, K, ldb):
+        flags |= PROJECT_COPY_B
+    s = ProjectShape(M, N, K, lda, ldb, max(out.stride(0), N), code, _type_of(out, "out"), flags)
+    L, need = lib(), ctypes.c_size_t(0)
+    _check(L.fkl_project_workspace_size(ctypes.byref(s), ctypes.byref(need)))
+    ws = _workspace(need.value, dev, workspace)
+    with _on(dev):
+        _check(L.fkl_project(ctypes.byref(s), a.data_ptr(), _ptr(a_scale), b.data_ptr(), b_scale.data_ptr(), _ptr(bias),
+                             out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev)))
+    return out
+
+
+def _setting(v, name, dtype, N, device):
+    """(pointer, shared value) of a sampling setting: a number, or a tensor with one for each row."""
+    if isinstance(v, _torch().Tensor):
+        _need(v, name, dtype, (N,), device)
+        return v.data_ptr(), 0
+    return None, v
+
+
+def sample_workspace_size(N, V, dtype=None) -> int:
+    """Workspace bytes of sample() for N rows of V logits (float32 unless dtype says otherwise)."""
+    s = SampleShape(N, V, V, V, _type_of(dtype or _torch().float32, "logits"))
+    b = ctypes.c_size_t(0)
+    _check(lib().fkl_sample_workspace_size(ctypes.byref(s), ctypes.byref(b)))
+    return b.value
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, token=None, logprob=None,
+           workspace=None):
+    """Draws one entry of each row of logits [N, V] (float32, bfloat16 or float16, rows contiguous) from
+    the random numbers u (fp32 [N], in [0, 1)), fkl_sample of include/fkl.h. temperature, top_k, top_p and
+    min_p are numbers, or tensors [N] with a value for each row (fp32; top_k int32). temperature 0 is
+    greedy; top_k <= 0, top_p >= 1 and min_p <= 0 are off. ids (int32 [N, V]) gives the vocabulary index of
+    each position, as topk() returns them with its logits. Returns (token int32 [N], logprob fp32 [N]): the
+    drawn entry and the log-probability it was drawn with; -1 and -inf for a row without an entry that is
+    neither -inf nor NaN."""
+    torch = _torch()
+    N, V, ld = _matrix(logits, "logits")
+    dev = logits.device
+    code = _type_of(logits, "logits")
+    _need(u, "u", torch.float32, (N,), dev)
+    f32 = torch.float32
+    T_rows, T = _setting(temperature, "temperature", f32, N, dev)
+    k_rows, k = _setting(top_k, "top_k", torch.int32, N, dev)
+    p_rows, p = _setting(top_p, "top_p", f32, N, dev)
+    q_rows, q = _setting(min_p, "min_p", f32, N, dev)
+    ld_ids = 0
+    if ids is not None:
+        n, v, ld_ids = _matrix(ids, "ids", dev)
+        if (n, v) != (N, V) or ids.dtype != torch.int32:
+            raise ValueError(f"ids must be int32 with shape {(N, V)}, got {ids.dtype} with {(n, v)}")
+    if token is None:
+        token = torch.empty(N, dtype=torch.int32, device=dev)
+    _need(token, "token", torch.int32, (N,), dev)
+    if logprob is None:
+        logprob = torch.empty(N, dtype=f32, device=dev)
+    _need(logprob, "logprob", f32, (N,), dev)
+    s = SampleShape(N, V, ld, ld_ids, code)
+    params = SampleParams(T_rows, k_rows, p_rows, q_rows, T, max(-1, min(int(k), V)), p, q)
+    L, need = lib(), ctypes.c_size_t(0)
+    _check(L.fkl_sample_workspace_size(ctypes.byref(s), ctypes.byref(need)))
+    ws = _workspace(need.value, dev, workspace)
+    with _on(dev):
+        _check(L.fkl_sample(ctypes.byref(s), ctypes.byref(params), logits.data_ptr(), _ptr(ids), u.data_ptr(),
+                            token.data_ptr(), logprob.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev)))
+    return token, logprob
 
 
 def trace_enable(on: bool = True) -> None:

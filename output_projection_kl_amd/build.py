@@ -25,7 +25,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libfkl.so")
 DEBUG_BUILD_DIR = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libfkl_debug.so")
 
-SOURCES = ["fkl_kernels.hip", "fkl_topk.hip", "fkl_api.cpp", "fkl_trace.cpp"]
+SOURCES = ["fkl_kernels.hip", "fkl_topk.hip", "fkl_int8.hip", "fkl_sample.hip", "fkl_api.cpp", "fkl_decode_api.cpp",
+           "fkl_trace.cpp"]
 ARCH = "gfx950"
 
 

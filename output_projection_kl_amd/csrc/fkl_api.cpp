@@ -68,6 +68,11 @@ fkl_status validate_if_asked(const fkl::Plan& p, const int32_t* t_idx, const flo
 
 namespace fkl {
 
+fkl_status set_error(fkl_status st, const std::string& msg) {
+  g_last_error = msg;
+  return st;
+}
+
 int grad_h_splits(int64_t rows, int64_t slab_w, int64_t d) {
   if (rows <= 0 || slab_w <= 0) return 1;
   const int64_t nb = ceil_div(d, kTile);

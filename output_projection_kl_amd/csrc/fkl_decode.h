@@ -1,0 +1,73 @@
+// Host-side plans and kernel launchers of the 8-bit head (fkl_quantize,
+// fkl_project) and of sampling (fkl_sample). Not part of the public interface.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fkl.h"
+#include "fkl_internal.h"
+
+namespace fkl {
+
+inline int type_bytes(int type) { return type == FKL_F32 ? 4 : type == FKL_I8 ? 1 : 2; }
+
+// Products of rows of up to this many 8-bit values cannot overflow a 32-bit
+// sum: 128 * 128 * K < 2^31.
+constexpr int64_t kProjectMaxK = 131071;
+
+// Debug build: access classes of these kernels, bits of the call's violation
+// word (at kDebugWordOffset in the workspace's first 256 bytes).
+enum DecodeDebugBit : uint32_t {
+  kDbgProjectOperand = 1u << 0,  // a, b, their packed copies, scales and bias
+  kDbgProjectOut = 1u << 1,      // the product
+  kDbgProjectWork = 1u << 2,     // the workspace: quantised or packed operands, partial sums
+  kDbgSampleLogits = 1u << 3,    // logits, ids, random numbers and per-row settings
+  kDbgSampleOut = 1u << 4,       // tokens and log-probabilities
+  kDbgSampleWork = 1u << 5,      // the workspace: per-row statistics
+};
+constexpr int kDecodeDebugBits = 6;
+
+struct ProjectPlan {
+  int64_t M, N, K, lda, ldb, ldo;
+  int a_type, out_type;
+  bool a_copied, b_copied;  // the 8-bit operand is copied to rows of round_up(K, 16) bytes
+  // workspace offsets (bytes): the quantised or copied a, its scales, the copied b
+  size_t off_a, off_a_scale, off_b, bytes;
+};
+
+struct ProjectArgs {
+  const void* a;
+  const float* a_scale;
+  const int8_t* b;
+  const float* b_scale;
+  const float* bias;
+  void* out;
+  char* ws;
+};
+
+struct SamplePlan {
+  int64_t N, V, ld, ld_ids;
+  int type;
+  size_t bytes;
+};
+
+struct SampleArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* u;
+  fkl_sample_params params;
+  int32_t* token;
+  float* logprob;
+  char* ws;
+};
+
+fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p);
+fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p);
+
+hipError_t launch_quantize(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
+                           float* scale, hipStream_t stream);
+hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& a, hipStream_t stream);
+hipError_t launch_sample(const SamplePlan& p, const SampleArgs& a, hipStream_t stream);
+
+}  // namespace fkl

@@ -1,0 +1,227 @@
+// C ABI of the 8-bit head and of sampling: argument checks (pure host code,
+// no HIP call before they pass), workspace plans, dispatch to the launchers in
+// fkl_int8.hip and fkl_sample.hip.
+#include <cmath>
+#include <string>
+
+#include "fkl.h"
+#include "fkl_decode.h"
+#include "fkl_internal.h"
+
+namespace {
+
+using fkl::set_error;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Row strides of 8-bit operands that the kernels read directly: whole 16-byte
+// pieces, and a tile's 256 rows within a 32-bit buffer size.
+bool readable_stride(int64_t ld) { return ld % 16 == 0 && ld <= (int64_t(1) << 22); }
+
+bool is_float_type(int t) { return t == FKL_F32 || t == FKL_BF16 || t == FKL_F16; }
+
+fkl_status check_workspace(const void* workspace, size_t given, size_t need, const char* size_call) {
+  if (!workspace) return set_error(FKL_EWORKSPACE, "workspace is NULL");
+  if (!aligned(workspace, 256)) return set_error(FKL_EWORKSPACE, "workspace must be 256-byte aligned");
+  if (given < need) return set_error(FKL_EWORKSPACE, std::string("workspace is smaller than ") + size_call);
+  return FKL_OK;
+}
+
+fkl_status launched(hipError_t e, const char* what) {
+  if (e == hipSuccess) return FKL_OK;
+  return set_error(FKL_EDEVICE, std::string(what) + " launch failed: " + hipGetErrorString(e));
+}
+
+// Debug build (FKL_DEBUG): the violation word of a call is cleared before its
+// first launch; after its last the host waits and reports what fired.
+fkl_status debug_begin(char* ws, hipStream_t stream) {
+#ifdef FKL_DEBUG
+  return launched(fkl::launch_debug_clear(reinterpret_cast<uint32_t*>(ws + fkl::kDebugWordOffset), stream),
+                  "debug word clear");
+#else
+  (void)ws, (void)stream;
+  return FKL_OK;
+#endif
+}
+
+fkl_status debug_end(char* ws, hipStream_t stream) {
+#ifdef FKL_DEBUG
+  static const char* const kNames[fkl::kDecodeDebugBits] = {"project operands", "project output",
+                                                            "project workspace", "sample inputs",
+                                                            "sample outputs",    "sample workspace"};
+  uint32_t host = 0;
+  hipError_t e = hipMemcpyAsync(&host, ws + fkl::kDebugWordOffset, sizeof(host), hipMemcpyDeviceToHost, stream);
+  if (e == hipSuccess) e = hipStreamSynchronize(stream);
+  if (e != hipSuccess) return launched(e, "debug word read");
+  if (host != 0) {
+    std::string msg = "device bounds check failed (accesses skipped):";
+    for (int b = 0; b < fkl::kDecodeDebugBits; ++b)
+      if (host & (1u << b)) msg += std::string(" ") + kNames[b] + ";";
+    return set_error(FKL_EDEVICE, msg);
+  }
+#else
+  (void)ws, (void)stream;
+#endif
+  return FKL_OK;
+}
+
+}  // namespace
+
+namespace fkl {
+
+fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p) {
+  if (!s) return set_error(FKL_EINVAL, "shape is NULL");
+  if (s->M < 0) return set_error(FKL_EINVAL, "M must be >= 0");
+  if (s->N < 1 || s->K < 1) return set_error(FKL_EINVAL, "N and K must be >= 1");
+  const int64_t kMax = (int64_t(1) << 31) - 1024;
+  if (s->M > kMax || s->N > kMax) return set_error(FKL_EUNSUPPORTED, "M and N must be < 2^31 - 1024");
+  if (s->K > kProjectMaxK)
+    return set_error(FKL_EUNSUPPORTED, "K must be <= 131071 (a 32-bit sum of 8-bit products could overflow)");
+  if (s->a_type != FKL_I8 && !is_float_type(s->a_type))
+    return set_error(FKL_EINVAL, "a_type must be FKL_I8, FKL_F32, FKL_BF16 or FKL_F16");
+  if (!is_float_type(s->out_type)) return set_error(FKL_EINVAL, "out_type must be FKL_F32, FKL_BF16 or FKL_F16");
+  if (s->lda < s->K || s->ldb < s->K) return set_error(FKL_EINVAL, "lda and ldb must be >= K");
+  if (s->ldo < s->N) return set_error(FKL_EINVAL, "ldo must be >= N");
+  const int64_t kMaxLd = int64_t(1) << 40;
+  if (s->lda > kMaxLd || s->ldb > kMaxLd || s->ldo > kMaxLd)
+    return set_error(FKL_EUNSUPPORTED, "lda, ldb and ldo must be <= 2^40");
+  if (s->flags & ~static_cast<uint32_t>(FKL_PROJECT_COPY_A | FKL_PROJECT_COPY_B))
+    return set_error(FKL_EINVAL, "unknown fkl_project_shape flag");
+  if (ceil_div(s->M, kTile) * ceil_div(s->N, kTile) >= (int64_t(1) << 22))
+    return set_error(FKL_EUNSUPPORTED, "out must hold fewer than 2^22 tiles of 256 x 256");
+  p->M = s->M, p->N = s->N, p->K = s->K;
+  p->lda = s->lda, p->ldb = s->ldb, p->ldo = s->ldo;
+  p->a_type = s->a_type, p->out_type = s->out_type;
+  p->a_copied = s->a_type == FKL_I8 && ((s->flags & FKL_PROJECT_COPY_A) || !readable_stride(s->lda));
+  p->b_copied = (s->flags & FKL_PROJECT_COPY_B) || !readable_stride(s->ldb);
+  const size_t row = static_cast<size_t>(round_up(s->K, 16));
+  size_t off = 256;
+  p->off_a = off;
+  if (p->a_copied || s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * row);
+  p->off_a_scale = off;
+  if (s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * 4);
+  p->off_b = off;
+  if (p->b_copied) off = align256(off + static_cast<size_t>(s->N) * row);
+  p->bytes = off;
+  return FKL_OK;
+}
+
+fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
+  if (!s) return set_error(FKL_EINVAL, "shape is NULL");
+  if (s->N < 0) return set_error(FKL_EINVAL, "N must be >= 0");
+  if (s->V < 1) return set_error(FKL_EINVAL, "V must be >= 1");
+  const int64_t kMax = (int64_t(1) << 31) - 1024;
+  if (s->N > kMax || s->V > kMax) return set_error(FKL_EUNSUPPORTED, "N and V must be < 2^31 - 1024");
+  if (!is_float_type(s->type)) return set_error(FKL_EINVAL, "type must be FKL_F32, FKL_BF16 or FKL_F16");
+  if (s->ld < s->V) return set_error(FKL_EINVAL, "ld must be >= V");
+  if (s->ld_ids < 0) return set_error(FKL_EINVAL, "ld_ids must be >= 0");
+  const int64_t kMaxLd = int64_t(1) << 40;
+  if (s->ld > kMaxLd || s->ld_ids > kMaxLd) return set_error(FKL_EUNSUPPORTED, "ld and ld_ids must be <= 2^40");
+  p->N = s->N, p->V = s->V, p->ld = s->ld, p->ld_ids = s->ld_ids;
+  p->type = s->type;
+  p->bytes = 256;
+  return FKL_OK;
+}
+
+}  // namespace fkl
+
+extern "C" {
+
+fkl_status fkl_quantize(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
+                        float* scale, void* stream) {
+  if (rows < 0) return set_error(FKL_EINVAL, "rows must be >= 0");
+  if (cols < 1) return set_error(FKL_EINVAL, "cols must be >= 1");
+  const int64_t kMax = (int64_t(1) << 31) - 1024;
+  if (rows > kMax || cols > kMax) return set_error(FKL_EUNSUPPORTED, "rows and cols must be < 2^31 - 1024");
+  if (!is_float_type(type)) return set_error(FKL_EINVAL, "type must be FKL_F32, FKL_BF16 or FKL_F16");
+  if (ldx < cols || ldq < cols) return set_error(FKL_EINVAL, "ldx and ldq must be >= cols");
+  const int64_t kMaxLd = int64_t(1) << 40;
+  if (ldx > kMaxLd || ldq > kMaxLd) return set_error(FKL_EUNSUPPORTED, "ldx and ldq must be <= 2^40");
+  if (rows == 0) return FKL_OK;
+  if (!x || !q || !scale) return set_error(FKL_EINVAL, "x, q and scale must not be NULL");
+  if (!aligned(x, fkl::type_bytes(type)) || !aligned(scale, 4))
+    return set_error(FKL_EINVAL, "x must be aligned to its type and scale to 4 bytes");
+  return launched(fkl::launch_quantize(rows, cols, type, x, ldx, q, ldq, scale, static_cast<hipStream_t>(stream)),
+                  "quantize");
+}
+
+fkl_status fkl_project_workspace_size(const fkl_project_shape* shape, size_t* bytes) {
+  fkl::ProjectPlan p;
+  const fkl_status st = fkl::make_project_plan(shape, &p);
+  if (st != FKL_OK) return st;
+  if (bytes) *bytes = p.bytes;
+  return FKL_OK;
+}
+
+fkl_status fkl_project(const fkl_project_shape* shape, const void* a, const float* a_scale, const int8_t* b,
+                       const float* b_scale, const float* bias, void* out, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  fkl::ProjectPlan p;
+  fkl_status st = fkl::make_project_plan(shape, &p);
+  if (st != FKL_OK) return st;
+  if (p.M == 0) return FKL_OK;
+  if (!a || !b || !b_scale || !out) return set_error(FKL_EINVAL, "a, b, b_scale and out must not be NULL");
+  if (p.a_type == FKL_I8 && !a_scale) return set_error(FKL_EINVAL, "a_scale must not be NULL with 8-bit rows");
+  if (p.a_type != FKL_I8 && a_scale)
+    return set_error(FKL_EINVAL, "a_scale must be NULL with floating rows: they are quantised by the call");
+  if (!aligned(a, fkl::type_bytes(p.a_type)) || !aligned(out, fkl::type_bytes(p.out_type)))
+    return set_error(FKL_EINVAL, "a and out must be aligned to their types");
+  if ((p.a_type == FKL_I8 && !p.a_copied && !aligned(a, 16)) || (!p.b_copied && !aligned(b, 16)))
+    return set_error(FKL_EINVAL, "an 8-bit operand that is read where it is must be 16-byte aligned "
+                                 "(FKL_PROJECT_COPY_A and FKL_PROJECT_COPY_B copy it first)");
+  if ((a_scale && !aligned(a_scale, 4)) || !aligned(b_scale, 4) || (bias && !aligned(bias, 4)))
+    return set_error(FKL_EINVAL, "a_scale, b_scale and bias must be 4-byte aligned");
+  st = check_workspace(workspace, workspace_bytes, p.bytes, "fkl_project_workspace_size()");
+  if (st != FKL_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = debug_begin(ws, s);
+  if (st != FKL_OK) return st;
+  const fkl::ProjectArgs args{a, a_scale, b, b_scale, bias, out, ws};
+  st = launched(fkl::launch_project(p, args, s), "project");
+  if (st != FKL_OK) return st;
+  return debug_end(ws, s);
+}
+
+fkl_status fkl_sample_workspace_size(const fkl_sample_shape* shape, size_t* bytes) {
+  fkl::SamplePlan p;
+  const fkl_status st = fkl::make_sample_plan(shape, &p);
+  if (st != FKL_OK) return st;
+  if (bytes) *bytes = p.bytes;
+  return FKL_OK;
+}
+
+fkl_status fkl_sample(const fkl_sample_shape* shape, const fkl_sample_params* params, const void* logits,
+                      const int32_t* ids, const float* u, int32_t* token, float* logprob, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  fkl::SamplePlan p;
+  fkl_status st = fkl::make_sample_plan(shape, &p);
+  if (st != FKL_OK) return st;
+  if (!params) return set_error(FKL_EINVAL, "params is NULL");
+  if (!params->temperature_rows && !(params->temperature >= 0.0f && std::isfinite(params->temperature)))
+    return set_error(FKL_EINVAL, "temperature must be finite and >= 0");
+  if (!params->top_p_rows && std::isnan(params->top_p)) return set_error(FKL_EINVAL, "top_p must not be NaN");
+  if (!params->min_p_rows && std::isnan(params->min_p)) return set_error(FKL_EINVAL, "min_p must not be NaN");
+  if (!aligned(params->temperature_rows, 4) || !aligned(params->top_k_rows, 4) || !aligned(params->top_p_rows, 4) ||
+      !aligned(params->min_p_rows, 4))
+    return set_error(FKL_EINVAL, "the per-row settings must be 4-byte aligned");
+  if (p.N == 0) return FKL_OK;
+  if (!logits || !u || !token) return set_error(FKL_EINVAL, "logits, u and token must not be NULL");
+  if (ids && p.ld_ids < p.V) return set_error(FKL_EINVAL, "ld_ids must be >= V");
+  if (!aligned(logits, fkl::type_bytes(p.type)) || !aligned(ids, 4) || !aligned(u, 4) || !aligned(token, 4) ||
+      !aligned(logprob, 4))
+    return set_error(FKL_EINVAL, "logits must be aligned to their type; ids, u, token and logprob to 4 bytes");
+  st = check_workspace(workspace, workspace_bytes, p.bytes, "fkl_sample_workspace_size()");
+  if (st != FKL_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = debug_begin(ws, s);
+  if (st != FKL_OK) return st;
+  const fkl::SampleArgs args{logits, ids, u, *params, token, logprob, ws};
+  st = launched(fkl::launch_sample(p, args, s), "sample");
+  if (st != FKL_OK) return st;
+  return debug_end(ws, s);
+}
+
+}  // extern "C"

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <string>
+
 #include "fkl.h"
 
 namespace fkl {
@@ -20,6 +22,9 @@ constexpr int64_t kDefaultSlabElems = int64_t(64) << 20;  // gradient block of ~
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int64_t ceil_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+// Sets the calling thread's fkl_last_error text and returns st.
+fkl_status set_error(fkl_status st, const std::string& msg);
 
 // Everything derived from the shape; computed on the host only.
 struct Plan {
