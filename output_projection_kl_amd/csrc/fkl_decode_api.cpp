@@ -120,7 +120,26 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   if (s->ld > kMaxLd || s->ld_ids > kMaxLd) return set_error(FKL_EUNSUPPORTED, "ld and ld_ids must be <= 2^40");
   p->N = s->N, p->V = s->V, p->ld = s->ld, p->ld_ids = s->ld_ids;
   p->type = s->type;
-  p->bytes = 256;
+  p->route = s->V <= kSampleScanMaxV ? kSampleScan : kSampleLong;
+  p->groups = p->chunks = p->chunk_elems = 0;
+  size_t off = 256;
+  p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
+  if (p->route == kSampleScan) {
+    // the larger chunks where they leave enough workgroups for every CU
+    p->chunk_elems = s->N * ceil_div(s->V, kSampleChunkLarge) >= 2 * kTargetBlocks ? kSampleChunkLarge
+                                                                                   : kSampleChunkSmall;
+    p->groups = ceil_div(s->V + 7, 64);
+    p->chunks = ceil_div(s->V + 7, p->chunk_elems);
+    const size_t n = static_cast<size_t>(s->N);
+    off = align256(off + n * p->groups * 4);
+    p->off_chunk_max = off;
+    off = align256(off + n * p->chunks * 4);
+    p->off_chunk_mass = off;
+    off = align256(off + n * p->chunks * 8);
+    p->off_chunk_hist = off;
+    off = align256(off + n * p->chunks * kSampleHistBytes);
+  }
+  p->bytes = off;
   return FKL_OK;
 }
 

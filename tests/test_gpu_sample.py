@@ -180,6 +180,40 @@ def test_sample_strided_rows_ids_and_given_outputs(V, dtype):
             assert (store[[0, 1, N + 2, N + 3]] == 77).all() and (lp[[0, 1, N + 2, N + 3]] == 77).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [262135, 262136, 262137, 300001])
+def test_sample_the_longest_rows(V, dtype):
+    """Around the row length at which the route changes, from aligned and unaligned rows."""
+    dev = _dev()
+    wide, u = _logits(3, V + 8, V, dtype, dev)
+    for lo in (0, 7):
+        x = wide[:, lo:lo + V]
+        for s in (dict(), dict(k=60), dict(k=5000, p=0.9), dict(p=0.9), dict(T=2.5, p=0.95), dict(q=0.01), dict(T=0.0)):
+            print(f"[sample] V={V} lo={lo} {dtype} {s}", flush=True)
+            _check(x, u, **s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,V", [(3, 60000), (40, 30000), (600, 20000)])
+def test_sample_flat_rows(N, V, dtype):
+    """Rows in which top-p keeps tens of thousands of entries, and rows whose
+    entries nearly all weigh the same."""
+    dev = _dev()
+    g = torch.Generator().manual_seed(N)
+    x = (torch.randn((N, V), generator=g) * torch.tensor([2.0, 1.0, 1e-3])[torch.arange(N) % 3][:, None] + 3.0).to(dtype)
+    x, u = x.to(dev), torch.rand(N, generator=g).to(dev)
+    rows = slice(0, 9)
+    for s in (dict(p=0.9), dict(p=0.999), dict(T=1.7, p=0.5), dict(p=0.95, q=1e-3), dict(k=6000), dict(k=V - 5, p=0.8)):
+        print(f"[sample] flat N={N} V={V} {dtype} {s}", flush=True)
+        token, logprob = fkl.sample(x, u, temperature=s.get("T", 1.0), top_k=s.get("k", 0), top_p=s.get("p", 1.0),
+                                    min_p=s.get("q", 0.0))
+        _check(x[rows], u[rows], **s)
+        few, few_logprob = fkl.sample(x[rows], u[rows], temperature=s.get("T", 1.0), top_k=s.get("k", 0),
+                                      top_p=s.get("p", 1.0), min_p=s.get("q", 0.0))
+        torch.cuda.synchronize()
+        assert torch.equal(token[rows], few) and torch.allclose(logprob[rows], few_logprob, rtol=1e-6, atol=1e-10)
+
+
 def test_sample_from_a_teacher_cache():
     """topk() lists, one entry drawn from each: the tokens are the lists' own indices."""
     dev = _dev()
