@@ -299,6 +299,33 @@ def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _enqueue(device, call, *args):
+    """call(*args, stream) with torch's current stream of `device`, that device current. As _on() and
+    _stream() around a call, without their cost where the device is current already: the calls of the
+    8-bit head and of sampling take microseconds on the GPU."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device.index:
+        _check(call(*args, _raw_stream(device.index)))
+    else:
+        with cuda.device(device):
+            _check(call(*args, _raw_stream(device.index)))
+
+
+def _raw_stream(index):
+    global _raw_stream
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the pointer without a Stream object around it
+    _raw_stream = get or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
+def _vector(t, name, dtype, n, device):
+    """_need() for a vector of n elements, its message looked for only where something is wrong."""
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.dim() == 1 and t.numel() == n and
+            t.device == device and t.is_contiguous()):
+        _need(t, name, dtype, (n,), device)
+
+
 def _on(device):
     """Makes `device` current for a library call (its kernels run on the current device)."""
     return _torch().cuda.device(device)
@@ -628,17 +655,21 @@ def quantize(x, q=None, scale=None):
     16 bytes, the layout that project() reads where it is (a view: q.stride(0) may exceed K)."""
     torch = _torch()
     M, K, ldx = _matrix(x, "x")
-    code = _type_of(x, "x")
+    code, dev = _type_of(x, "x"), x.device
     if q is None:
-        q = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=x.device)[:, :K]
-    if _matrix(q, "q", x.device)[:2] != (M, K) or q.dtype != torch.int8:
-        raise ValueError(f"q must be int8 with shape {(M, K)}, got {q.dtype} with {tuple(q.shape)}")
+        ldq = -(-K // 16) * 16
+        q = torch.empty((M, ldq), dtype=torch.int8, device=dev)
+        if ldq != K:
+            q = q[:, :K]
+    else:
+        rows, cols, ldq = _matrix(q, "q", dev)
+        if (rows, cols) != (M, K) or q.dtype != torch.int8:
+            raise ValueError(f"q must be int8 with shape {(M, K)}, got {q.dtype} with {(rows, cols)}")
     if scale is None:
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _need(scale, "scale", torch.float32, (M,), x.device)
-    with _on(x.device):
-        _check(lib().fkl_quantize(M, K, code, x.data_ptr(), ldx, q.data_ptr(), max(q.stride(0), K), scale.data_ptr(),
-                                  _stream(x.device)))
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+    else:
+        _vector(scale, "scale", torch.float32, M, dev)
+    _enqueue(dev, lib().fkl_quantize, M, K, code, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr())
     return q, scale
 
 
@@ -651,7 +682,8 @@ def _read_where_it_is(t, rows, cols, ld):
     last 16-byte piece inside the tensor's storage."""
     if ld % 16 or t.data_ptr() % 16:
         return False
-    return rows == 0 or t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16 <= t.untyped_storage().nbytes()
+    return cols % 16 == 0 or rows == 0 or (
+        t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16 <= t.untyped_storage().nbytes())
 
 
 def project_workspace_size(M, N, K, a_dtype=None, out_dtype=None, lda=None, ldb=None, ldo=None, flags=0) -> int:
@@ -674,6 +706,7 @@ def project(a, b, b_scale, a_scale=None, bias=None, out_dtype=None, out=None, wo
     bias: fp32 [N]. Rows may be strided; int8 rows that are not 16-byte aligned are copied first. For
     inference: no gradient flows through it."""
     torch = _torch()
+    f32 = torch.float32
     M, K, lda = _matrix(a, "a")
     dev = a.device
     N, Kb, ldb = _matrix(b, "b", dev)
@@ -682,38 +715,39 @@ def project(a, b, b_scale, a_scale=None, bias=None, out_dtype=None, out=None, wo
     if Kb != K:
         raise ValueError(f"a and b must have the same number of columns, got {K} and {Kb}")
     code = _type_of(a, "a", True)
-    _need(b_scale, "b_scale", torch.float32, (N,), dev)
+    _vector(b_scale, "b_scale", f32, N, dev)
     if (a_scale is None) != (code != _I8):
         raise ValueError("a_scale goes with an int8 a; a floating a is quantised by the call")
     if a_scale is not None:
-        _need(a_scale, "a_scale", torch.float32, (M,), dev)
+        _vector(a_scale, "a_scale", f32, M, dev)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (N,), dev)
+        _vector(bias, "bias", f32, N, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    if _matrix(out, "out", dev)[:2] != (M, N):
-        raise ValueError(f"out must have shape {(M, N)}, got {tuple(out.shape)}")
+        out, ldo = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev), N
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        rows, cols, ldo = _matrix(out, "out", dev)
+        if (rows, cols) != (M, N):
+            raise ValueError(f"out must have shape {(M, N)}, got {(rows, cols)}")
     flags = 0
     if code == _I8 and not _read_where_it_is(a, M, K, lda):
         flags |= PROJECT_COPY_A
     if not _read_where_it_is(b, N, K, ldb):
         flags |= PROJECT_COPY_B
-    s = ProjectShape(M, N, K, lda, ldb, max(out.stride(0), N), code, _type_of(out, "out"), flags)
+    s = ctypes.byref(ProjectShape(M, N, K, lda, ldb, ldo, code, _type_of(out, "out"), flags))
     L, need = lib(), ctypes.c_size_t(0)
-    _check(L.fkl_project_workspace_size(ctypes.byref(s), ctypes.byref(need)))
+    _check(L.fkl_project_workspace_size(s, ctypes.byref(need)))
     ws = _workspace(need.value, dev, workspace)
-    with _on(dev):
-        _check(L.fkl_project(ctypes.byref(s), a.data_ptr(), _ptr(a_scale), b.data_ptr(), b_scale.data_ptr(), _ptr(bias),
-                             out.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev)))
+    _enqueue(dev, L.fkl_project, s, a.data_ptr(), None if a_scale is None else a_scale.data_ptr(), b.data_ptr(),
+             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), ws.data_ptr(), _nbytes(ws))
     return out
 
 
 def _setting(v, name, dtype, N, device):
     """(pointer, shared value) of a sampling setting: a number, or a tensor with one for each row."""
     if isinstance(v, _torch().Tensor):
-        _need(v, name, dtype, (N,), device)
+        _vector(v, name, dtype, N, device)
         return v.data_ptr(), 0
     return None, v
 
@@ -739,8 +773,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, 
     N, V, ld = _matrix(logits, "logits")
     dev = logits.device
     code = _type_of(logits, "logits")
-    _need(u, "u", torch.float32, (N,), dev)
     f32 = torch.float32
+    _vector(u, "u", f32, N, dev)
     T_rows, T = _setting(temperature, "temperature", f32, N, dev)
     k_rows, k = _setting(top_k, "top_k", torch.int32, N, dev)
     p_rows, p = _setting(top_p, "top_p", f32, N, dev)
@@ -752,18 +786,19 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, 
             raise ValueError(f"ids must be int32 with shape {(N, V)}, got {ids.dtype} with {(n, v)}")
     if token is None:
         token = torch.empty(N, dtype=torch.int32, device=dev)
-    _need(token, "token", torch.int32, (N,), dev)
+    else:
+        _vector(token, "token", torch.int32, N, dev)
     if logprob is None:
         logprob = torch.empty(N, dtype=f32, device=dev)
-    _need(logprob, "logprob", f32, (N,), dev)
-    s = SampleShape(N, V, ld, ld_ids, code)
+    else:
+        _vector(logprob, "logprob", f32, N, dev)
+    s = ctypes.byref(SampleShape(N, V, ld, ld_ids, code))
     params = SampleParams(T_rows, k_rows, p_rows, q_rows, T, max(-1, min(int(k), V)), p, q)
     L, need = lib(), ctypes.c_size_t(0)
-    _check(L.fkl_sample_workspace_size(ctypes.byref(s), ctypes.byref(need)))
+    _check(L.fkl_sample_workspace_size(s, ctypes.byref(need)))
     ws = _workspace(need.value, dev, workspace)
-    with _on(dev):
-        _check(L.fkl_sample(ctypes.byref(s), ctypes.byref(params), logits.data_ptr(), _ptr(ids), u.data_ptr(),
-                            token.data_ptr(), logprob.data_ptr(), ws.data_ptr(), _nbytes(ws), _stream(dev)))
+    _enqueue(dev, L.fkl_sample, s, ctypes.byref(params), logits.data_ptr(), None if ids is None else ids.data_ptr(),
+             u.data_ptr(), token.data_ptr(), logprob.data_ptr(), ws.data_ptr(), _nbytes(ws))
     return token, logprob
 
 

@@ -46,18 +46,21 @@ struct ProjectArgs {
   char* ws;
 };
 
-enum SampleRoute { kSampleScan, kSampleLong };
+enum SampleRoute { kSampleShort, kSampleScan, kSampleLong };
 
 struct SamplePlan {
   int64_t N, V, ld, ld_ids;
   int type;
   SampleRoute route;
-  // the scan: groups of 64 elements and chunks of chunk_elems per row, counted
-  // with the up to 7 elements between a 16-byte boundary and the row's start
+  // the scan: groups of 2^group_shift elements and chunks of chunk_elems per
+  // row, counted with the up to 7 elements between a 16-byte boundary and the
+  // row's start
   int64_t groups, chunks, chunk_elems;
+  int group_shift;
   size_t off_group_max, off_chunk_max, off_chunk_mass, off_chunk_hist, bytes;
 };
 
+constexpr int64_t kSampleShortMaxV = 1024;
 constexpr int64_t kSampleScanMaxV = (int64_t(1) << 18) - 8;
 constexpr int64_t kSampleChunkSmall = 4096;   // elements per scan workgroup where there are few rows
 constexpr int64_t kSampleChunkLarge = 16384;

@@ -120,15 +120,18 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   if (s->ld > kMaxLd || s->ld_ids > kMaxLd) return set_error(FKL_EUNSUPPORTED, "ld and ld_ids must be <= 2^40");
   p->N = s->N, p->V = s->V, p->ld = s->ld, p->ld_ids = s->ld_ids;
   p->type = s->type;
-  p->route = s->V <= kSampleScanMaxV ? kSampleScan : kSampleLong;
-  p->groups = p->chunks = p->chunk_elems = 0;
+  p->route = s->V <= kSampleShortMaxV ? kSampleShort : s->V <= kSampleScanMaxV ? kSampleScan : kSampleLong;
+  p->groups = p->chunks = p->chunk_elems = p->group_shift = 0;
   size_t off = 256;
   p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
   if (p->route == kSampleScan) {
     // the larger chunks where they leave enough workgroups for every CU
     p->chunk_elems = s->N * ceil_div(s->V, kSampleChunkLarge) >= 2 * kTargetBlocks ? kSampleChunkLarge
                                                                                    : kSampleChunkSmall;
-    p->groups = ceil_div(s->V + 7, 64);
+    // the smaller groups as long as a row has at most 4096 of them: top-k's
+    // bound, the k-th largest group maximum, needs many more groups than k
+    p->group_shift = s->V + 7 <= 4096 * 16 ? 4 : 6;
+    p->groups = ceil_div(s->V + 7, int64_t(1) << p->group_shift);
     p->chunks = ceil_div(s->V + 7, p->chunk_elems);
     const size_t n = static_cast<size_t>(s->N);
     off = align256(off + n * p->groups * 4);

@@ -44,10 +44,77 @@ __device__ __forceinline__ float key_logit(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// 2^t in fp64 for t <= 0: t = n + f with |f| <= 1/2, the Taylor series of
-// exp(f ln 2) to the 12th power (remainder below 0.3466^13 / 13! = 1.7e-16).
-// Below the smallest normal number the result is 0.
-__device__ __forceinline__ double exp2_neg(double t) {
+// Cross-lane moves within a wave by DPP: lane i receives the value of the lane
+// that CTRL names, 0 where there is none or its row is not in ROWS.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{dpp<CTRL, ROWS>(w[0]), dpp<CTRL, ROWS>(w[1])});
+}
+
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{from_lane(w[0], lane), from_lane(w[1], lane)});
+}
+
+// Inclusive running sums over the wave: within each row of 16 lanes by shifts
+// of 1, 2, 4 and 8, then the row ends carried over (lane 15 of a row into the
+// next, lane 31 into the upper half).
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += dpp<0x111>(v);
+  v += dpp<0x112>(v);
+  v += dpp<0x114>(v);
+  v += dpp<0x118>(v);
+  v += dpp<0x142, 0xa>(v);
+  v += dpp<0x143, 0xc>(v);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp<0x111>(v));
+  v = max(v, dpp<0x112>(v));
+  v = max(v, dpp<0x114>(v));
+  v = max(v, dpp<0x118>(v));
+  v = max(v, dpp<0x142, 0xa>(v));
+  v = max(v, dpp<0x143, 0xc>(v));
+  return from_lane(v, 63);
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) { return from_lane(wave_scan(v), 63); }
+
+// The value of lane (this lane ^ X).
+template <int X>
+__device__ __forceinline__ uint32_t xor_lane(uint32_t v) {
+  static_assert(X == 1 || X == 2 || X == 4 || X == 8 || X == 16 || X == 32, "one bit");
+  if constexpr (X == 1) return dpp<0xb1>(v);                 // pairs swapped
+  else if constexpr (X == 2) return dpp<0x4e>(v);            // pairs of pairs swapped
+  else if constexpr (X == 4) return dpp<0x1b>(dpp<0x141>(v));  // mirrored in eights, then in fours
+  else if constexpr (X == 8) return dpp<0x128>(v);           // rotated by 8 of 16
+  else if constexpr (X == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32) ? r[0] : r[1];
+  }
+}
+
+template <int X>
+__device__ __forceinline__ float xor_lane_f32(float v) {
+  return __uint_as_float(xor_lane<X>(__float_as_uint(v)));
+}
+
+// 2^t in fp64: t = n + f with |f| <= 1/2, the Taylor series of exp(f ln 2) to
+// the 12th power (remainder below 0.3466^13 / 13! = 1.7e-16). 0 below 2^-1022.
+__device__ __forceinline__ double exp2_f64(double t) {
   if (!(t > -1022.0)) return 0.0;
   const double n = rint(t);
   const double y = (t - n) * 0.69314718055994530942;
@@ -67,13 +134,35 @@ __device__ __forceinline__ double exp2_neg(double t) {
   return ldexp(s, static_cast<int>(n));
 }
 
+// 2^(t / 16) split for the scan, which takes one of every entry: t = b + f with
+// b the nearest integer (found by adding and subtracting 1.5 * 2^52, whose sum
+// holds b in its low word; |t| < 2^31) and |f| <= 1/2; 2^(f / 16) by Taylor's
+// series to the 5th power (remainder below 0.0217^6 / 6! = 1.5e-13).
+struct Sixteenths {
+  int b;
+  double f;
+  __device__ __forceinline__ explicit Sixteenths(double t) {
+    const double r = t + 6755399441055744.0;
+    b = static_cast<int>(__double2loint(r));
+    f = t - (r - 6755399441055744.0);
+  }
+  __device__ __forceinline__ double fraction() const {
+    constexpr double g = 0.69314718055994530942 / 16.0;
+    double s = fma(g * g * g * g * g / 120.0, f, g * g * g * g / 24.0);
+    s = fma(s, f, g * g * g / 6.0);
+    s = fma(s, f, g * g / 2.0);
+    s = fma(s, f, g);
+    return fma(s, f, 1.0);
+  }
+};
+
 // Geometry of the scan. A row is read in 16-byte pieces at 16-byte aligned
 // addresses: element e of the row's pieces is position e - lead, lead the
 // elements between the aligned address and the row's start.
-constexpr int kGroup = 64;                 // elements per recorded maximum
 constexpr int kScanElems = 16;             // elements per thread of a scan workgroup
 constexpr int kScanBins = 512;             // mass histogram: bins of 1/16 bit below the chunk's maximum
-constexpr int kCandidates = 4096;          // entries that k_sample_pick settles in LDS
+constexpr int kCandidates = 4096;          // entries that k_sample_pick settles in LDS,
+constexpr int kWaveCandidates = 1024;       // and how many of them by one wave
 constexpr int kShortRow = 1024;
 
 struct SampleParams {
@@ -93,7 +182,7 @@ struct SampleParams {
   uint32_t* chunk_max;
   double* chunk_mass;
   uint64_t* chunk_hist;
-  int32_t groups, chunks, chunk_elems;
+  int32_t groups, group_shift, chunks, chunk_elems;
   DebugCheck dbg;  // debug build: span 0 = logits, 1 = ids, 2 = u, 3 = token, 4 = logprob
 };
 
@@ -101,7 +190,7 @@ struct SampleParams {
 struct RowSettings {
   bool valid;
   double c;     // log2(e) / T
-  uint32_t k;   // entries kept at most; V when off
+  uint32_t k;   // entries kept at most; 2^31 - 1 when off
   double p;     // >= 1 when off
   double q;     // <= 0 when off
   double u;
@@ -117,7 +206,7 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& P, int64
   s.valid = T >= 0.0f && T < INFINITY;
   // the first entry alone: greedy, or a filter that only it can pass
   const bool first = T == 0.0f || p <= 0.0f || q > 1.0f;
-  s.k = first ? 1u : (k <= 0 || k > P.V) ? static_cast<uint32_t>(P.V) : static_cast<uint32_t>(k);
+  s.k = first ? 1u : (k <= 0 || k >= P.V) ? 0x7fffffffu : static_cast<uint32_t>(k);
   s.c = T > 0.0f ? 1.4426950408889634074 / static_cast<double>(T) : 1.0;
   s.p = first || !(p < 1.0f) ? 1.0 : static_cast<double>(p);
   s.q = first || !(q > 0.0f) ? 0.0 : static_cast<double>(q);
@@ -140,15 +229,7 @@ __device__ __forceinline__ RowMode row_mode(const RowSettings& s, int V) {
 __device__ __forceinline__ double weight_of(uint32_t key, float m, uint32_t m_key, double c) {
   if (key == m_key) return 1.0;
   if (key <= kMaskedKey) return 0.0;
-  return exp2_neg((static_cast<double>(key_logit(key)) - static_cast<double>(m)) * c);
-}
-
-__device__ __forceinline__ double shfl_xor_f64(double v, int mask) { return __shfl_xor(v, mask, 64); }
-
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += shfl_xor_f64(v, o);
-  return v;
+  return exp2_f64((static_cast<double>(key_logit(key)) - static_cast<double>(m)) * c);
 }
 
 // The first position of [0, V) at which the running sum of weight(position)
@@ -196,12 +277,7 @@ __device__ int find_position(Weight weight, int V, double target, double* shared
       continue;
     }
     if (wave == at) {
-      double incl = mine;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(incl, o, 64);
-        if (lane >= o) incl += y;
-      }
+      const double incl = wave_scan(mine);
       const uint64_t hit = __ballot(mine > 0.0 && at_base + incl > target);
       const uint64_t any = __ballot(mine > 0.0);
       const int l = hit ? __ffsll(static_cast<long long>(hit)) - 1 : 63 - __clzll(static_cast<long long>(any));
@@ -376,70 +452,78 @@ struct RowView {
     lead = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   }
 
-  // Keys of piece i; 0 (below every logit's key) for elements outside the row.
-  __device__ __forceinline__ void piece(const DebugCheck& dbg, int i, uint32_t (&key)[kPer]) const {
+  // Piece i as it lies in memory; -inf in place of elements outside the row.
+  __device__ __forceinline__ u32x4 raw(const DebugCheck& dbg, int i) const {
     const int first = i * kPer - lead;
-    if (first >= 0 && first + kPer <= V) {
-      const u32x4 v = dload(dbg, 0, kDbgSampleLogits, reinterpret_cast<const u32x4*>(x + first));
+    if (first >= 0 && first + kPer <= V) return dload(dbg, 0, kDbgSampleLogits, reinterpret_cast<const u32x4*>(x + first));
+    u32x4 v;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const uint32_t w = v[j * sizeof(T) / 4];
-        key[j] = logit_key(logit_of_bits<T>(sizeof(T) == 4 ? w : (j & 1) ? w >> 16 : w & 0xffffu));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int at = first + j;
-        key[j] = at >= 0 && at < V ? logit_key(static_cast<float>(dload(dbg, 0, kDbgSampleLogits, x + at))) : 0u;
-      }
+    for (int j = 0; j < kPer; ++j) {
+      const int at = first + j;
+      const T e = at >= 0 && at < V ? dload(dbg, 0, kDbgSampleLogits, x + at) : static_cast<T>(-INFINITY);
+      if constexpr (sizeof(T) == 4) v[j] = __builtin_bit_cast(uint32_t, e);
+      else if (j & 1) v[j / 2] |= static_cast<uint32_t>(__builtin_bit_cast(uint16_t, e)) << 16;
+      else v[j / 2] = __builtin_bit_cast(uint16_t, e);
     }
+    return v;
+  }
+
+  static __device__ __forceinline__ float logit(const u32x4& v, int j) {
+    const uint32_t w = v[j * sizeof(T) / 4];
+    return logit_of_bits<T>(sizeof(T) == 4 ? w : (j & 1) ? w >> 16 : w & 0xffffu);
+  }
+
+  // The same as logits.
+  __device__ __forceinline__ void logits(const DebugCheck& dbg, int i, float (&v)[kPer]) const {
+    const u32x4 w = raw(dbg, i);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] = logit(w, j);
   }
 
   __device__ __forceinline__ uint32_t element(const DebugCheck& dbg, int e) const {
-    const int at = e - lead;
+    const int at = e - lead;  // before the row for a negative e
     return at >= 0 && at < V ? logit_key(static_cast<float>(dload(dbg, 0, kDbgSampleLogits, x + at))) : 0u;
   }
 };
 
-// The mass histogram's grid: entry x lies in bin floor(16 x log2(e) / T), a
-// monotone function of x; its weight relative to the bin's lower edge is
-// 2^(f / 16), f the fraction: exp(y) by Taylor's series to the 6th power, y <=
-// ln(2) / 16 (remainder below 6e-14).
-__device__ __forceinline__ double bin_weight(double f) {
-  const double y = f * (0.69314718055994530942 / 16.0);
-  double s = fma(1.0 / 720.0, y, 1.0 / 120.0);
-  s = fma(s, y, 1.0 / 24.0);
-  s = fma(s, y, 1.0 / 6.0);
-  s = fma(s, y, 0.5);
-  s = fma(s, y, 1.0);
-  return fma(s, y, 1.0);
-}
-
-// A histogram word: entries counted from bit 49 up, below it their weights in
-// units of 2^-34 (16384 entries of at most 2^(1/16) stay below 2^49). The
-// rounding is 2^-35 of a weight, either way: over n entries the sums are off
-// by sqrt(n) 2^-35 of a weight, and a draw differs from that of exact sums
-// with a probability below 1e-8 at 2^18 entries.
+// The mass histogram's grid: entry x lies in bin rint(16 x log2(e) / T), a
+// monotone function of x, with the weight 2^(f / 16) relative to the bin's
+// centre. A histogram word holds the number of entries from bit 49 up, and
+// below it their weights in units of 2^-34 (16384 entries of at most 2^(1/32)
+// stay below 2^49). The rounding is 2^-35 of a weight either way: over n
+// entries the sums are off by sqrt(n) 2^-35 of a weight, and a draw differs
+// from that of exact sums with a probability below 1e-8 at 2^18 entries.
+// Integer sums do not depend on their order.
 constexpr int kHistShift = 34;
 constexpr int kHistCount = 49;
-constexpr double kMaxBin = 16777216.0;  // larger |bin| numbers: left to sample_row_exact
+constexpr double kMaxBin = 16777216.0;  // rows beyond it are left to sample_row_exact
 
 __device__ __forceinline__ uint32_t hist_count(uint64_t w) { return static_cast<uint32_t>(w >> kHistCount); }
-__device__ __forceinline__ double hist_mass(uint64_t w) {
-  return static_cast<double>(w & ((uint64_t(1) << kHistCount) - 1)) * (1.0 / (uint64_t(1) << kHistShift));
+__device__ __forceinline__ uint64_t hist_units(uint64_t w) { return w & ((uint64_t(1) << kHistCount) - 1); }
+__device__ __forceinline__ double units_mass(uint64_t units) {
+  return static_cast<double>(units) * (1.0 / (uint64_t(1) << kHistShift));
+}
+
+// One entry's histogram word: its weight is rounded to units by adding 1.5 *
+// 2^18, whose last place is 2^-34.
+__device__ __forceinline__ uint64_t hist_word(const Sixteenths& x) {
+  constexpr uint64_t kBits = 0x4118000000000000ull;  // of 1.5 * 2^18
+  return static_cast<uint64_t>(__double_as_longlong(x.fraction() + 393216.0)) +
+         ((uint64_t(1) << kHistCount) - kBits);
 }
 
 // One workgroup per chunk of a row. HBM bound where only the maxima are
-// wanted; with the masses, the fp64 arithmetic of one exponential per entry
-// takes about as long as the reading.
+// wanted; with the masses, one fp64 exponential per entry (about 17 vector
+// instructions, and an LDS atomic for the histogram) takes longer than the
+// reading.
 template <class T, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   constexpr int kPer = RowView<T>::kPer;
   constexpr int kPieces = kScanElems / kPer;
   constexpr int kWaves = kThreads / 64;
-  constexpr int kLanes = kGroup / kPer;  // lanes that share a group
   __shared__ uint64_t hist[kScanBins];
-  __shared__ uint32_t wave_max[kWaves];
+  __shared__ double sixteenth[16];
+  __shared__ float wave_top[kWaves];
   __shared__ double wave_mass[kWaves];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -447,62 +531,79 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   const int64_t row = P.row0 + blockIdx.x / P.chunks;
   const RowView<T> view(P, row);
   const int64_t slot = row * P.chunks + chunk;
-  uint32_t key[kPieces][kPer];
+  float x[kPieces][kPer];
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) view.piece(P.dbg, chunk * (kThreads * kPieces) + p * kThreads + tid, key[p]);
+  for (int p = 0; p < kPieces; ++p) view.logits(P.dbg, chunk * (kThreads * kPieces) + p * kThreads + tid, x[p]);
   const RowSettings S = row_settings(P, row);
   const RowMode mode = row_mode(S, P.V);
-  uint32_t top = 0;
+  float top = -INFINITY;
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
-    uint32_t m = key[p][0];
+    float m = -INFINITY;  // a NaN is no maximum
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) m = max(m, key[p][j]);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), o, 64)));
-    const int g = (chunk * (kThreads * kScanElems) + (p * kThreads + tid) * kPer) / kGroup;
-    if (lane % kLanes == 0 && g < P.groups)
-      dstore(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + g, m);
-    top = max(top, m);
+    for (int j = 0; j < kPer; ++j) m = fmaxf(m, x[p][j]);
+    // the maximum of 16, then of 64 consecutive elements
+    const int e = chunk * (kThreads * kScanElems) + (p * kThreads + tid) * kPer;
+    m = fmaxf(m, xor_lane_f32<1>(m));
+    if constexpr (kPer == 4) m = fmaxf(m, xor_lane_f32<2>(m));
+    if (P.group_shift == 4 && e % 16 == 0 && e / 16 < P.groups)
+      dstore(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + e / 16, logit_key(m));
+    if constexpr (kPer == 8) m = fmaxf(m, xor_lane_f32<2>(m));
+    m = fmaxf(m, xor_lane_f32<4>(m));
+    if constexpr (kPer == 4) m = fmaxf(m, xor_lane_f32<8>(m));
+    if (P.group_shift == 6 && e % 64 == 0 && e / 64 < P.groups)
+      dstore(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + e / 64, logit_key(m));
+    top = fmaxf(top, m);
   }
   if (mode == kMaximaOnly) return;
-#pragma unroll
-  for (int o = 32; o >= kLanes; o >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o, 64)));
-  if (lane == 0) wave_max[tid >> 6] = top;
+  if constexpr (kPer == 8) top = fmaxf(top, xor_lane_f32<8>(top));
+  top = fmaxf(top, xor_lane_f32<16>(top));
+  top = fmaxf(top, xor_lane_f32<32>(top));
+  if (lane == 0) wave_top[tid >> 6] = top;
   if (mode == kMassHistogram)
     for (int i = tid; i < kScanBins; i += kThreads) hist[i] = 0;
+  else if (tid < 16)
+    sixteenth[tid] = exp2_f64(tid * (1.0 / 16.0));
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) top = max(top, wave_max[w]);
-  const float m = key_logit(top);
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, wave_top[w]);
+  const double c16 = 16.0 * S.c;
   double sum = 0.0;
   if (mode == kChunkMass) {
-    if (top > kMaskedKey) {
+    if (top == INFINITY) {
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += weight_of(key[p][j], m, top, S.c);
-    }
-  } else {
-    const double c16 = 16.0 * S.c;
-    const double base = floor(static_cast<double>(m) * c16);
-    if (top > kMaskedKey && fabs(base) < kMaxBin) {
+        for (int j = 0; j < kPer; ++j) sum += x[p][j] == INFINITY ? 1.0 : 0.0;
+    } else if (top > -INFINITY) {
+      // 2^(t / 16) as the fraction's power, a sixteenth's and an exponent; what
+      // lies 2^-1000 below the chunk's largest (masked entries among it) adds
+      // as much as nothing
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          if (key[p][j] <= kMaskedKey) continue;
-          const double t = static_cast<double>(key_logit(key[p][j])) * c16;
-          const double b = floor(t);
-          const double d = base - b;
-          if (d < kScanBins) {
-            const uint64_t w = static_cast<uint64_t>(bin_weight(t - b) * (uint64_t(1) << kHistShift) + 0.5);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&hist[static_cast<int>(d)]),
-                      static_cast<unsigned long long>((uint64_t(1) << kHistCount) + w));
-          } else {
-            // 2^-32 of the chunk's largest weight or less: fp32's relative precision is enough
+          const Sixteenths e(fmax((static_cast<double>(x[p][j]) - static_cast<double>(top)) * c16, -16000.0));
+          const double w = e.fraction() * sixteenth[e.b & 15];
+          sum += __hiloint2double(__double2hiint(w) + ((e.b >> 4) << 20), __double2loint(w));
+        }
+    }
+  } else {
+    const double base = rint(static_cast<double>(top) * c16);
+    if (fabs(base) < kMaxBin) {
+      const int first = static_cast<int>(base);
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          // masked entries and what lies 2^-256 below the chunk's largest: all in one place, of no weight
+          const double t = fmax(static_cast<double>(x[p][j]) * c16, base - 4096.0);
+          const Sixteenths e(t);
+          const uint32_t d = static_cast<uint32_t>(first - e.b);
+          if (d < kScanBins)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&hist[d]), static_cast<unsigned long long>(hist_word(e)));
+          else  // 2^-32 of the chunk's largest weight or less: fp32's relative precision is enough
             sum += static_cast<double>(exp2f(static_cast<float>((t - base) * (1.0 / 16.0))));
-          }
         }
     }
     __syncthreads();
@@ -515,13 +616,13 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   if (tid == 0) {
     double s = 0.0;
     for (int w = 0; w < kWaves; ++w) s += wave_mass[w];
-    dstore(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot, top);
+    dstore(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot, logit_key(top));
     dstore(P.dbg, 5, kDbgSampleWork, P.chunk_mass + slot, s);
   }
 }
 
-constexpr int kMaxGroups = (1 << 18) / kGroup + 1;
-constexpr int kMaxChunks = (1 << 18) / (256 * kScanElems) + 1;
+constexpr int kMaxGroups = 4096;
+constexpr int kMaxChunks = 64;
 
 struct PickLds {
   uint32_t group_max[kMaxGroups];
@@ -531,53 +632,38 @@ struct PickLds {
       int32_t pos[kCandidates];
     } cand;
     uint64_t entry[kCandidates];  // (key, ~position) of the border bin's entries
+    struct {
+      uint32_t count[kScanBins];
+      double mass[kScanBins];
+    } half;  // the second half of the block's sums over the chunks
   };
   union {
     uint32_t sorted[kCandidates];
     uint32_t bins[kRowThreads];
     uint32_t list[kCandidates];  // groups that reach the bound
+    uint64_t sub[kRowThreads];   // the border bin's finer histogram
   };
-  double chunk[kMaxChunks + 1];
-  double wave_f64[kRowWaves];
-  uint32_t wave_u32[kRowWaves];
-  uint32_t word[4];
+  double bin_scale[kScanBins];  // 2^(-d / 16)
+  double sixteenth[16];         // 2^(j / 16)
+  double chunk[kMaxChunks];
+  uint64_t chunk_units[kMaxChunks];
+  int32_t chunk_off[kMaxChunks];
+  double wave_f64[6][kRowWaves];
+  uint32_t wave_u32[6][kRowWaves];
+  uint32_t word[10];
   double value[2];
+  uint64_t edge;
+  uint32_t few[64];
 };
 
-// Exclusive sum of v over the block in thread order; total gets the sum.
-__device__ __forceinline__ double block_scan_f64(double v, double* wave, double& total) {
-  const int lane = threadIdx.x & 63;
-  double incl = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double y = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += y;
-  }
+// Exclusive sum of v over the block in thread order; total gets the sum. One
+// barrier: `wave` must not have been in use since the last one.
+template <class V>
+__device__ __forceinline__ V block_scan(V v, V* wave, V& total) {
+  const V incl = wave_scan(v);
+  if ((threadIdx.x & 63) == 63) wave[threadIdx.x >> 6] = incl;
   __syncthreads();
-  if (lane == 63) wave[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  double base = 0.0, sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) {
-    if (w == static_cast<int>(threadIdx.x >> 6)) base = sum;
-    sum += wave[w];
-  }
-  total = sum;
-  return base + (incl - v);
-}
-
-__device__ __forceinline__ uint32_t block_scan_u32(uint32_t v, uint32_t* wave, uint32_t& total) {
-  const int lane = threadIdx.x & 63;
-  uint32_t incl = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t y = static_cast<uint32_t>(__shfl_up(static_cast<int>(incl), o, 64));
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();
-  if (lane == 63) wave[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  uint32_t base = 0, sum = 0;
+  V base = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < kRowWaves; ++w) {
     if (w == static_cast<int>(threadIdx.x >> 6)) base = sum;
@@ -589,8 +675,7 @@ __device__ __forceinline__ uint32_t block_scan_u32(uint32_t v, uint32_t* wave, u
 
 // Sorts n keys (LDS, room for the next power of two >= 64) in descending order;
 // the keys past n are 0.
-template <class K>
-__device__ void sort_descending(K* a, int n) {
+__device__ void sort_descending(uint32_t* a, int n) {
   int size = 64;
   while (size < n) size <<= 1;
   const int tid = threadIdx.x;
@@ -600,7 +685,7 @@ __device__ void sort_descending(K* a, int n) {
     for (int j = k >> 1; j > 0; j >>= 1) {
       for (int p = tid; p < size / 2; p += kRowThreads) {
         const int i = 2 * p - (p & (j - 1));
-        const K x = a[i], y = a[i + j];
+        const uint32_t x = a[i], y = a[i + j];
         if ((x < y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
       }
       __syncthreads();
@@ -608,8 +693,157 @@ __device__ void sort_descending(K* a, int n) {
   }
 }
 
-// Upper bound on the distance from the largest key for the bins of
-// bound_of_kth: exact below 32, then 32 bins per power of two.
+// One compare-exchange step of a wave's bitonic sort (descending) of 64 R keys,
+// lane l holding elements l R .. l R + R - 1.
+template <int R, int K, int J>
+__device__ __forceinline__ void sort_step(uint32_t (&s)[R]) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (J < R) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r & J) continue;
+      const uint32_t hi = max(s[r], s[r | J]), lo = min(s[r], s[r | J]);
+      const bool down = K < R ? (r & K) == 0 : (lane & (K / R)) == 0;
+      s[r] = down ? hi : lo;
+      s[r | J] = down ? lo : hi;
+    }
+  } else {
+    const bool take_max = ((lane & (J / R)) == 0) == ((lane & (K / R)) == 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t o = xor_lane<J / R>(s[r]);
+      s[r] = take_max ? max(s[r], o) : min(s[r], o);
+    }
+  }
+  if constexpr (J > 1) sort_step<R, K, J / 2>(s);
+}
+
+template <int R, int K = 2>
+__device__ __forceinline__ void sort_wave(uint32_t (&s)[R]) {
+  sort_step<R, K, K / 2>(s);
+  if constexpr (K < 64 * R) sort_wave<R, 2 * K>(s);
+}
+
+// Border and draw among 64 R entries held by one wave, entry l R + r in lane l
+// (keys at or below kMaskedKey: none). whole: the mass that top-p goes by, or
+// negative for that of the first k entries. Returns the entry drawn, prob its
+// probability, to every lane. At least one entry must be unmasked.
+template <int R>
+__device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSettings& S, float m, uint32_t m_key,
+                                           double whole, double& prob) {
+  const int lane = threadIdx.x & 63;
+  uint32_t edge = kMaskedKey + 1;
+  uint32_t quota = 0xffffffffu;  // of the entries equal to the edge, the first this many are kept
+  uint32_t ties = 0;
+  double w[R];
+  const bool ordered = S.k < 64 * R || S.p < 1.0;
+  if (ordered) {
+    uint32_t s[R];
+    bool falls = true;  // already in order, as a teacher cache's lists are
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = key[r];
+      if (r > 0) falls = falls && key[r - 1] >= key[r];
+    }
+    const uint32_t next = dpp<0x130>(key[0]);  // of the following lane; 0 at the end
+    falls = falls && key[R - 1] >= next;
+    if (__ballot(falls) != ~uint64_t(0)) sort_wave<R>(s);
+    double mine = 0.0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[r] = static_cast<uint32_t>(lane * R + r) < S.k ? weight_of(s[r], m, m_key, S.c) : 0.0;
+      mine += w[r];
+    }
+    const double incl = wave_scan(mine);
+    const double target = S.p * (whole < 0.0 ? from_lane(incl, 63) : whole);
+    double run = incl - mine;
+    uint32_t n_kept = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool keep = static_cast<uint32_t>(lane * R + r) < S.k && s[r] > kMaskedKey &&
+                        (S.p >= 1.0 || run < target) && w[r] >= S.q;
+      n_kept += __popcll(__ballot(keep));
+      run += w[r];
+    }
+    const uint32_t last = n_kept > 0 ? n_kept - 1 : 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r == static_cast<int>(last % R)) edge = from_lane(s[r], static_cast<int>(last / R));
+    uint32_t above = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      above += __popcll(__ballot(s[r] > edge));
+      ties += __popcll(__ballot(s[r] == edge));
+    }
+    quota = last + 1 - above;
+  }
+  uint32_t before = 0;
+  if (quota < ties) {  // the border falls inside a group of equal entries
+    uint32_t mine = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) mine += key[r] == edge;
+    before = wave_scan(mine) - mine;
+  } else {
+    quota = 0xffffffffu;
+  }
+  double mine = 0.0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool in = key[r] > edge || (key[r] == edge && before++ < quota);
+    w[r] = in ? weight_of(key[r], m, m_key, S.c) : 0.0;
+    if (!ordered && w[r] < S.q) w[r] = 0.0;
+    mine += w[r];
+  }
+  const double incl = wave_scan(mine);
+  const double kept = from_lane(incl, 63);
+  const double goal = S.u * kept;
+  double run = incl - mine;
+  int hit = R, last = 0;
+  double w_hit = 0.0, w_last = 0.0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    run += w[r];
+    if (w[r] > 0.0) {
+      if (hit == R && run > goal) hit = r, w_hit = w[r];
+      last = r, w_last = w[r];
+    }
+  }
+  const uint64_t hits = __ballot(hit < R);
+  const uint64_t any = __ballot(w_last > 0.0);
+  const int l = hits ? __ffsll(static_cast<long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(any));
+  prob = (hits ? from_lane(w_hit, l) : from_lane(w_last, l)) / kept;
+  return l * R + static_cast<int>(from_lane(static_cast<uint32_t>(hits ? hit : last), l));
+}
+
+// Rows of up to 64 R entries, one wave each: latency of one row's chain of
+// steps for few rows, vector instructions (about 700 for R = 2) for many.
+template <class T, int R>
+__global__ __launch_bounds__(256) void k_sample_short(SampleParams P, int64_t rows) {
+  const int lane = threadIdx.x & 63;
+  const int64_t local = blockIdx.x * 4ll + (threadIdx.x >> 6);
+  if (local >= rows) return;
+  const int64_t row = P.row0 + local;
+  const T* x = static_cast<const T*>(P.logits) + row * P.ld;
+  uint32_t key[R], m_key = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int at = lane * R + r;
+    key[r] = at < P.V ? logit_key(static_cast<float>(dload(P.dbg, 0, kDbgSampleLogits, x + at))) : 0u;
+    m_key = max(m_key, key[r]);
+  }
+  m_key = wave_max_u32(m_key);
+  const RowSettings S = row_settings(P, row);
+  if (!S.valid || m_key <= kMaskedKey) {
+    if (lane == 0) put_none(P, row);
+    return;
+  }
+  double prob;
+  const int at = settle_wave<R>(key, S, key_logit(m_key), m_key, -1.0, prob);
+  if (lane == 0) put_draw(P, row, at, prob);
+}
+
+// Distance of a key from the largest, in bins for bound_of_kth: exact below
+// 32, then 32 bins per power of two.
 __device__ __forceinline__ uint32_t distance_bin(uint32_t d) {
   if (d < 32) return d;
   const int e = 31 - __clz(static_cast<int>(d));
@@ -623,7 +857,7 @@ __device__ __forceinline__ uint32_t distance_bin_end(uint32_t b) {
 
 // A key that at least k of the row's entries reach: at least k group maxima
 // do. kMaskedKey + 1 where fewer than k groups hold an unmasked entry.
-__device__ uint32_t bound_of_kth(PickLds& L, int groups, uint32_t m_key, uint32_t k) {
+__device__ __forceinline__ uint32_t bound_of_kth(PickLds& L, int groups, uint32_t m_key, uint32_t k) {
   const int tid = threadIdx.x;
   L.bins[tid] = 0;
   if (tid == 0) L.word[0] = kMaskedKey + 1;
@@ -633,80 +867,372 @@ __device__ uint32_t bound_of_kth(PickLds& L, int groups, uint32_t m_key, uint32_
   __syncthreads();
   const uint32_t mine = L.bins[tid];
   uint32_t total;
-  const uint32_t before = block_scan_u32(mine, L.wave_u32, total);
+  const uint32_t before = block_scan(mine, L.wave_u32[1], total);
   if (before < k && before + mine >= k) {
     const uint32_t d = distance_bin_end(static_cast<uint32_t>(tid));
     L.word[0] = max(kMaskedKey + 1, d < m_key ? m_key - d : 0u);
   }
   __syncthreads();
-  const uint32_t bound = L.word[0];
-  __syncthreads();
-  return bound;
+  return L.word[0];
 }
 
-// The draw within one chunk: the first position at which base plus the kept
-// weights up to it exceeds target; weight(key, position) is 0 for what is not
-// kept. Returns the position and its weight to every thread.
+// The lowest key in (kMaskedKey, m_key] whose bin is at least b; m_key + 1 if
+// there is none. Each step tests 64 keys of the range, one per lane.
+__device__ __forceinline__ uint32_t first_key_of_bin(double b, double c16, uint32_t m_key) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint64_t lo = kMaskedKey + 1, hi = static_cast<uint64_t>(m_key) + 1;
+  while (lo < hi) {
+    const uint64_t step = (hi - lo) / 64 + 1;
+    const uint64_t at = lo + lane * step;
+    const bool in = at >= hi || rint(static_cast<double>(key_logit(static_cast<uint32_t>(at))) * c16) >= b;
+    const uint64_t hit = __ballot(in);
+    const int f = hit ? __ffsll(static_cast<long long>(hit)) - 1 : 64;
+    if (f < 64) hi = min(hi, lo + f * step);
+    if (f > 0) lo = lo + (f - 1) * step + 1;
+    else hi = lo;
+  }
+  return static_cast<uint32_t>(lo);
+}
+
+// 2^(t / 16) for t <= 16, by the table L.sixteenth; 0 below 2^-1000.
+__device__ __forceinline__ double power(const PickLds& L, double t) {
+  const Sixteenths e(fmax(t, -16000.0));
+  const double w = e.fraction() * L.sixteenth[e.b & 15];
+  const double v = __hiloint2double(__double2hiint(w) + ((e.b >> 4) << 20), __double2loint(w));
+  return t < -16000.0 ? 0.0 : v;
+}
+
+// The draw within one chunk, from the first position at which base plus the
+// kept weights up to it exceeds goal; weight(logit, position) is 0 for what is
+// not kept (masked entries among it), kept the sum over the row.
 template <class T, class Weight>
-__device__ int draw_in_chunk(const SampleParams& P, const RowView<T>& view, PickLds& L, int chunk, double base,
-                             double target, Weight weight, double& w_at) {
+__device__ __forceinline__ void draw_in_chunk(const SampleParams& P, int64_t row, const RowView<T>& view, PickLds& L,
+                                              int chunk, double base, double goal, double kept, Weight weight) {
   constexpr int kPer = RowView<T>::kPer;
   const int tid = threadIdx.x;
   const int pieces = P.chunk_elems / kPer;
+  __syncthreads();
   if (tid == 0) L.word[0] = 0xffffffffu, L.word[1] = 0;
+  int first_at = -1, last_at = -1;  // this thread's positions past the goal, and of positive weight
+  double first_w = 0.0, last_w = 0.0;
   for (int p0 = 0; p0 < pieces; p0 += kRowThreads) {
-    uint32_t key[kPer];
+    float x[kPer];
     double w[kPer], sum = 0.0, total;
     const int piece = chunk * pieces + p0 + tid;
+    const int pos = piece * kPer - view.lead;
     const bool live = p0 + tid < pieces;
-    if (live) view.piece(P.dbg, piece, key);
-    int last = -1;
+    if (live) view.logits(P.dbg, piece, x);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      w[j] = live ? weight(key[j], piece * kPer - view.lead + j) : 0.0;
+      w[j] = live ? weight(x[j], pos + j) : 0.0;
       sum += w[j];
-      if (w[j] > 0.0) last = j;
+      if (w[j] > 0.0) last_at = pos + j, last_w = w[j];
     }
-    const double before = base + block_scan_f64(sum, L.wave_f64, total);
+    __syncthreads();
+    double run = base + block_scan(sum, L.wave_f64[5], total);
     if (sum > 0.0) {
-      double run = before;
-      int at = -1;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         run += w[j];
-        if (at < 0 && w[j] > 0.0 && run > target) at = j;
+        if (first_at < 0 && w[j] > 0.0 && run > goal) first_at = pos + j, first_w = w[j];
       }
-      const uint32_t pos = static_cast<uint32_t>(piece * kPer - view.lead);
-      if (at >= 0) atomicMin(&L.word[0], pos + at);
-      atomicMax(&L.word[1], pos + last);  // if rounding leaves no such position: the last one kept
+      if (first_at >= 0) atomicMin(&L.word[0], static_cast<uint32_t>(first_at));
+      atomicMax(&L.word[1], static_cast<uint32_t>(last_at));
     }
     base += total;
     __syncthreads();
     if (L.word[0] != 0xffffffffu) break;
   }
-  const int at = static_cast<int>(L.word[0] != 0xffffffffu ? L.word[0] : L.word[1]);
-  w_at = weight(logit_key(static_cast<float>(dload(P.dbg, 0, kDbgSampleLogits, view.x + at))), at);
-  __syncthreads();
+  // if rounding leaves no such position, the last one kept
+  const bool found = L.word[0] != 0xffffffffu;
+  const int at = static_cast<int>(found ? L.word[0] : L.word[1]);
+  if (found ? first_at == at : last_at == at) put_draw(P, row, at, (found ? first_w : last_w) / kept);
+}
+
+// The chunk in which the running sum of L.chunk[0 .. n), n <= 64, exceeds the
+// share u of its total (the last one that is not empty if rounding leaves
+// none); total, goal = u total, and the sum before the chunk.
+__device__ __forceinline__ int find_chunk(const PickLds& L, int n, double u, double& total, double& goal,
+                                          double& base) {
+  const int lane = threadIdx.x & 63;
+  const double w = lane < n ? L.chunk[lane] : 0.0;
+  const double incl = wave_scan(w);
+  total = from_lane(incl, 63);
+  goal = u * total;
+  const uint64_t any = __ballot(w > 0.0);
+  const uint64_t hit = __ballot(w > 0.0 && incl > goal);
+  const int at = hit ? __ffsll(static_cast<long long>(hit)) - 1 : 63 - __clzll(static_cast<long long>(any));
+  base = from_lane(incl - w, at);
   return at;
 }
 
-// The chunk in which the running sum of L.chunk[0 .. n) exceeds target (the
-// last one that is not empty if rounding leaves none); base: the sum before it.
-__device__ int find_chunk(const PickLds& L, int n, double target, double& base) {
-  int at = 0;
-  double run = 0.0;
-  bool found = false;
-  base = 0.0;
-  for (int i = 0; i < n; ++i) {
-    const double w = L.chunk[i];
-    if (!found && w > 0.0) {
-      at = i;
-      base = run;
-      found = run + w > target;
-    }
-    run += w;
+// What the mass histograms say of a row.
+struct RowHistogram {
+  double c16, base;   // the grid, and the bin of the row's largest logit
+  double whole;       // the row's mass relative to 2^(base / 16)
+  uint32_t border;    // the bin (from the top) in which the mass reaches target
+  uint32_t in_border, above;  // entries in it and above it
+  double mass_above;
+  double target;
+};
+
+// Adds up a row's histograms and finds the border bin; false where it lies
+// below the bins.
+__device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slot, const RowSettings& S, float m,
+                                              PickLds& L, RowHistogram& H) {
+  const int tid = threadIdx.x;
+  H.c16 = 16.0 * S.c;
+  H.base = rint(static_cast<double>(m) * H.c16);
+  if (!(fabs(H.base) < kMaxBin)) return false;
+  double rest = 0.0;
+  if (tid < P.chunks) {
+    const uint32_t ck = dload(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot + tid);
+    const double cm = dload(P.dbg, 5, kDbgSampleWork, P.chunk_mass + slot + tid);
+    // chunk bin i is row bin i + off; a masked chunk's are all empty
+    const double off = ck > kMaskedKey ? H.base - rint(static_cast<double>(key_logit(ck)) * H.c16) : 1e6;
+    L.chunk_off[tid] = static_cast<int>(fmin(off, 1e6));
+    rest = cm * power(L, -off);
   }
-  return at;
+  if (tid < kScanBins) L.bin_scale[tid] = power(L, -tid);
+  if (tid == 0) L.word[2] = 0xffffffffu;
+  __syncthreads();
+  // the block's two halves take every second chunk
+  const int bin = tid % kScanBins;
+  uint32_t count = 0;
+  double mass = 0.0;
+#pragma unroll 4
+  for (int ch = tid / kScanBins; ch < P.chunks; ch += kRowThreads / kScanBins) {
+    const int off = L.chunk_off[ch];
+    const bool inside = off <= bin;  // otherwise a chunk bin below the row's last
+    const int i = off >= kScanBins ? bin : inside ? bin - off : bin - off + kScanBins;
+    const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + i);
+    const double v = units_mass(hist_units(w));
+    if (inside) count += hist_count(w), mass += v;
+    else if (w) rest += v * power(L, -(off + i));
+  }
+  if (tid >= kScanBins) L.half.count[bin] = count, L.half.mass[bin] = mass;
+  __syncthreads();
+  if (tid < kScanBins) count += L.half.count[bin], mass += L.half.mass[bin];
+  else count = 0, mass = 0.0;
+  const double scaled = tid < kScanBins ? mass * L.bin_scale[bin] : 0.0;
+  double in_bins, rest_all;
+  uint32_t counted;
+  const double above = block_scan(scaled, L.wave_f64[0], in_bins);
+  block_scan(rest, L.wave_f64[1], rest_all);
+  const uint32_t count_above = block_scan(count, L.wave_u32[2], counted);
+  H.whole = in_bins + rest_all;
+  H.target = S.p * H.whole;
+  if (count > 0 && above < H.target && above + scaled >= H.target) atomicMin(&L.word[2], static_cast<uint32_t>(tid));
+  __syncthreads();
+  H.border = L.word[2];
+  if (H.border == 0xffffffffu) return false;
+  if (static_cast<uint32_t>(tid) == H.border) L.word[3] = count, L.word[4] = count_above, L.value[0] = above;
+  __syncthreads();
+  H.in_border = L.word[3];
+  H.above = L.word[4];
+  H.mass_above = L.value[0];
+  return true;
+}
+
+// A row of which top-p keeps more entries than one wave settles: the
+// bins above the border are kept whole, and only the border bin's entries are
+// gathered (one read of the row), counted into 1024 finer bins, and settled
+// there: a few entries by comparing them all, many equal ones by their
+// positions. false where neither is the case.
+template <class T>
+__device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row, const RowSettings& S,
+                                              const RowView<T>& view, uint32_t m_key, PickLds& L,
+                                              const RowHistogram& H) {
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = tid >> 6;
+  const int V = P.V;
+  const int64_t slot = row * P.chunks;
+  if (H.in_border > kCandidates) return false;
+  const int n = static_cast<int>(H.in_border);
+  const double edge_bin = H.base - H.border;
+  if (wave < 2) {
+    const uint32_t key = first_key_of_bin(edge_bin + wave, H.c16, m_key);
+    if (lane == 0) L.word[wave] = key;
+  }
+  __syncthreads();
+  const uint32_t k_lo = L.word[0], k_hi = L.word[1];
+  const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
+  const int sub_shift = max(0, 22 - __clz(static_cast<int>((k_hi - k_lo - 1) | 1)));
+  auto units = [&](uint32_t key) {
+    return hist_units(hist_word(Sixteenths(static_cast<double>(key_logit(key)) * H.c16)));
+  };
+  const double scale = L.bin_scale[H.border] * (1.0 / (uint64_t(1) << kHistShift));  // of the border bin's units
+  __syncthreads();
+  L.sub[tid] = 0;
+  if (tid < P.chunks) L.chunk_units[tid] = 0;
+  if (tid == 0) L.word[0] = 0, L.word[5] = 0, L.word[6] = 0, L.word[7] = 0xffffffffu, L.word[8] = 0;
+  __syncthreads();
+  constexpr int kPer = RowView<T>::kPer;
+  const int pieces = (view.lead + V + kPer - 1) / kPer;
+  auto take = [&](float x, int pos) {
+    const uint32_t key = logit_key(x);
+    const uint32_t at = atomicAdd(&L.word[0], 1u);
+    if (at < kCandidates) L.entry[at] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(pos));
+    atomicAdd(reinterpret_cast<unsigned long long*>(&L.sub[min((key - k_lo) >> sub_shift, 1023u)]),
+              static_cast<unsigned long long>((uint64_t(1) << kHistCount) + units(key)));
+  };
+  constexpr int kBatch = 4;  // pieces read before any is looked at
+  for (int i0 = tid; i0 < pieces; i0 += kBatch * kRowThreads) {
+    u32x4 held[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) held[b] = view.raw(P.dbg, i0 + b * kRowThreads);  // -inf past the row
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float x = view.logit(held[b], j);
+        hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << j;
+      }
+      if (hits) {
+        const int pos = (i0 + b * kRowThreads) * kPer - view.lead;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (hits >> j & 1) take(view.logit(held[b], j), pos + j);
+      }
+    }
+  }
+  __syncthreads();
+  // the finer bin at which the mass reaches the target (the last one if rounding leaves none)
+  const uint64_t word = L.sub[kRowThreads - 1 - tid];
+  const uint32_t count = hist_count(word);
+  const double mass = static_cast<double>(hist_units(word)) * scale;
+  double sum;
+  const double above = H.mass_above + block_scan(mass, L.wave_f64[2], sum);
+  if (count > 0 && (above < H.target || tid == 0)) atomicMax(&L.word[5], static_cast<uint32_t>(tid));
+  __syncthreads();
+  const uint32_t sub = kRowThreads - 1 - L.word[5];
+  if (static_cast<uint32_t>(tid) == L.word[5]) L.word[9] = count, L.value[1] = above;
+  __syncthreads();
+  const int n_sub = static_cast<int>(L.word[9]);
+  const double above_sub = L.value[1];
+  if (n_sub <= 64) {
+    for (int i = tid; i < n; i += kRowThreads)
+      if (min((static_cast<uint32_t>(L.entry[i] >> 32) - k_lo) >> sub_shift, 1023u) == sub)
+        L.few[atomicAdd(&L.word[6], 1u)] = static_cast<uint32_t>(i);
+    __syncthreads();
+    if (wave == 0) {
+      const uint64_t mine = lane < n_sub ? L.entry[L.few[lane]] : 0;
+      uint64_t before = 0;
+      uint64_t edge = ~uint64_t(0);
+      for (int i = 0; i < n_sub; ++i) {
+        const uint64_t other = (static_cast<uint64_t>(from_lane(static_cast<uint32_t>(mine >> 32), i)) << 32) |
+                               from_lane(static_cast<uint32_t>(mine), i);
+        if (other > mine) before += units(static_cast<uint32_t>(other >> 32));
+      }
+      const bool keep = lane < n_sub && (before == 0 || above_sub + static_cast<double>(before) * scale < H.target);
+      for (uint64_t left = __ballot(keep); left; left &= left - 1) {
+        const int i = __ffsll(static_cast<long long>(left)) - 1;
+        const uint64_t other = (static_cast<uint64_t>(from_lane(static_cast<uint32_t>(mine >> 32), i)) << 32) |
+                               from_lane(static_cast<uint32_t>(mine), i);
+        edge = min(edge, other);
+      }
+      if (lane == 0) L.edge = edge;
+    }
+  } else {
+    // many entries: settled only if they are all equal
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint32_t key = static_cast<uint32_t>(L.entry[i] >> 32);
+      if (min((key - k_lo) >> sub_shift, 1023u) == sub) atomicMin(&L.word[7], key), atomicMax(&L.word[8], key);
+    }
+    L.few[lane] = 0;
+    __syncthreads();
+    const uint32_t key = L.word[7];
+    if (key != L.word[8]) return false;
+    const double each = static_cast<double>(units(key)) * scale;
+    const double want = ceil((H.target - above_sub) / each);
+    const uint32_t quota = want < 1.0 ? 1u : want > n_sub ? static_cast<uint32_t>(n_sub) : static_cast<uint32_t>(want);
+    // the quota-th of their positions: by bins of 2^pos_shift positions, then a bitmap of the bin
+    int pos_shift = 0;
+    while ((V - 1) >> pos_shift >= kRowThreads) ++pos_shift;
+    L.bins[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kRowThreads)
+      if (static_cast<uint32_t>(L.entry[i] >> 32) == key)
+        atomicAdd(&L.bins[(0xffffffffu - static_cast<uint32_t>(L.entry[i])) >> pos_shift], 1u);
+    __syncthreads();
+    const uint32_t here = L.bins[tid];
+    uint32_t all;
+    const uint32_t before = block_scan(here, L.wave_u32[3], all);
+    if (before < quota && before + here >= quota) L.word[3] = static_cast<uint32_t>(tid), L.word[4] = quota - before;
+    __syncthreads();
+    const uint32_t pos_bin = L.word[3];
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint32_t pos = 0xffffffffu - static_cast<uint32_t>(L.entry[i]);
+      if (static_cast<uint32_t>(L.entry[i] >> 32) == key && pos >> pos_shift == pos_bin) {
+        const uint32_t bit = pos & ((1u << pos_shift) - 1);
+        atomicOr(&L.few[bit >> 5], 1u << (bit & 31));
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t nth = L.word[4], pos = pos_bin << pos_shift;
+      for (int i = 0; i < 8; ++i) {
+        uint32_t bits = L.few[i];
+        const uint32_t c = static_cast<uint32_t>(__popc(bits));
+        if (nth > c) {
+          nth -= c;
+          continue;
+        }
+        while (--nth > 0) bits &= bits - 1;
+        pos += static_cast<uint32_t>(i * 32 + __ffs(static_cast<int>(bits)) - 1);
+        break;
+      }
+      L.edge = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - pos);
+    }
+  }
+  __syncthreads();
+  const uint64_t edge = L.edge;
+  const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
+  const int edge_pos = static_cast<int>(0xffffffffu - static_cast<uint32_t>(edge));
+  // each chunk's kept mass: its bins above the border, and its kept entries of the border bin
+  for (int i = tid; i < n; i += kRowThreads) {
+    const uint64_t e = L.entry[i];
+    if (e >= edge) {
+      const int at = static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) + view.lead;
+      atomicAdd(reinterpret_cast<unsigned long long*>(&L.chunk_units[at / P.chunk_elems]),
+                static_cast<unsigned long long>(units(static_cast<uint32_t>(e >> 32))));
+    }
+  }
+  __syncthreads();
+  const int border = static_cast<int>(H.border);
+  for (int ch = wave; ch < P.chunks; ch += kRowWaves) {
+    const int off = L.chunk_off[ch];
+    double s = 0.0;
+#pragma unroll 4
+    for (int d = lane; d < border - off; d += 64) {
+      const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + d);
+      s += units_mass(hist_units(w)) * L.bin_scale[off + d];
+    }
+    s = wave_sum_f64(s);
+    if (lane == 0) L.chunk[ch] = s + static_cast<double>(L.chunk_units[ch]) * scale;
+  }
+  __syncthreads();
+  double kept, goal, before;
+  const int chunk = find_chunk(L, P.chunks, S.u, kept, goal, before);
+  const float edge_x = key_logit(edge_key);
+  draw_in_chunk(P, row, view, L, chunk, before, goal, kept, [&](float x, int pos) {
+    return x > edge_x || (x == edge_x && pos <= edge_pos) ? power(L, static_cast<double>(x) * H.c16 - H.base) : 0.0;
+  });
+  return true;
+}
+
+template <int R>
+__device__ __forceinline__ void settle_candidates(const SampleParams& P, int64_t row, const RowSettings& S, float m,
+                                                  uint32_t m_key, const PickLds& L, int n, double whole) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) key[r] = lane * R + r < n ? L.cand.key[lane * R + r] : 0u;
+  double prob;
+  const int at = settle_wave<R>(key, S, m, m_key, whole, prob);
+  if (lane == 0) put_draw(P, row, L.cand.pos[at], prob);
 }
 
 // Settles a row from what the scan left; false where the border is too wide
@@ -721,8 +1247,9 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   const RowMode mode = row_mode(S, V);
   const float m = key_logit(m_key);
   const int64_t slot = row * P.chunks;
-  // the whole row's mass relative to m
-  double total = 0.0;
+  const bool all = S.k >= static_cast<uint32_t>(V);  // top-k is off
+
+  double whole = -1.0;  // the mass that top-p goes by, relative to m; negative: that of the first k entries
   if (mode == kChunkMass) {
     if (tid < P.chunks) {
       const uint32_t ck = dload(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot + tid);
@@ -730,22 +1257,21 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
       L.chunk[tid] = ck > kMaskedKey ? cm * weight_of(ck, m, m_key, S.c) : 0.0;
     }
     __syncthreads();
-    for (int i = 0; i < P.chunks; ++i) total += L.chunk[i];
-    if (S.p >= 1.0 && S.q <= 0.0) {  // no filter: a chunk, then a position in it
-      double base, w;
-      const double target = S.u * total;
-      const int chunk = find_chunk(L, P.chunks, target, base);
-      const int at = draw_in_chunk(P, view, L, chunk, base, target,
-                                   [&](uint32_t key, int) { return weight_of(key, m, m_key, S.c); }, w);
-      if (tid == 0) put_draw(P, row, at, w / total);
+    double goal, base;
+    const int chunk = find_chunk(L, P.chunks, S.u, whole, goal, base);
+    if (S.p >= 1.0) {  // no filter: a chunk, then a position in it
+      draw_in_chunk(P, row, view, L, chunk, base, goal, whole, [&](float x, int) {
+        const double d = x == m ? 0.0 : static_cast<double>(x) - static_cast<double>(m);  // m may be infinite
+        return x > -INFINITY ? power(L, d * (16.0 * S.c)) : 0.0;
+      });
       return true;
     }
   }
 
   // a key that every kept entry reaches
   uint32_t bound = kMaskedKey + 1;
-  if (S.k < static_cast<uint32_t>(V)) bound = S.k == 1 ? m_key : bound_of_kth(L, P.groups, m_key, S.k);
-  if (S.q > 0.0 && isfinite(m) && (S.p >= 1.0 || S.k >= static_cast<uint32_t>(V))) {
+  if (!all) bound = S.k == 1 ? m_key : bound_of_kth(L, P.groups, m_key, S.k);
+  if (S.q > 0.0 && isfinite(m) && (S.p >= 1.0 || all)) {
     // w >= q: x >= m + log2(q) / c, taken lower by more than its rounding
     // (top-p after top-k needs the mass of all the k entries: no bound from q then)
     const double lo = static_cast<double>(m) + log2(S.q) / S.c;
@@ -753,143 +1279,11 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     bound = max(bound, logit_key(low));
   }
   if (mode == kMassHistogram) {
-    const double c16 = 16.0 * S.c;
-    const double t_max = static_cast<double>(m) * c16;
-    const double base = floor(t_max);
-    if (!(fabs(base) < kMaxBin)) return false;
-    // bin d (from the top) of the row, and the mass below the last bin
-    uint32_t cnt = 0;
-    double mass = 0.0, rest = 0.0;
-    for (int ch = 0; ch < P.chunks; ++ch) {
-      const uint32_t ck = dload(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot + ch);
-      if (ck <= kMaskedKey) continue;
-      const double cb = floor(static_cast<double>(key_logit(ck)) * c16);
-      const double off = base - cb;  // >= 0: the chunk's bins start this much lower
-      if (tid < kScanBins) {
-        const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + tid);
-        // added up below through LDS: chunk bin tid is row bin tid + off
-        const double d = off + tid;
-        if (w) {
-          if (d < kScanBins) {
-            if (off == 0.0) cnt += hist_count(w), mass += hist_mass(w);
-          } else {
-            rest += hist_mass(w) * exp2_neg(-d * (1.0 / 16.0));
-          }
-        }
-        const int src = tid - static_cast<int>(off < kScanBins ? off : kScanBins);
-        if (off > 0.0 && off < kScanBins && src >= 0) {
-          const uint64_t v = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + src);
-          cnt += hist_count(v), mass += hist_mass(v);
-        }
-      }
-      if (tid == kScanBins)
-        rest += dload(P.dbg, 5, kDbgSampleWork, P.chunk_mass + slot + ch) * exp2_neg(-off * (1.0 / 16.0));
-    }
-    const double scaled = mass * exp2_neg(-tid * (1.0 / 16.0));  // relative to 2^(base / 16)
-    double in_bins, rest_all;
-    const double above = block_scan_f64(scaled, L.wave_f64, in_bins);
-    block_scan_f64(rest, L.wave_f64, rest_all);
-    uint32_t counted;
-    const uint32_t cnt_above = block_scan_u32(cnt, L.wave_u32, counted);
-    const double whole = in_bins + rest_all;
-    const double target = S.p * whole;
-    if (tid == 0) L.word[1] = 0xffffffffu;
-    __syncthreads();
-    if (cnt > 0 && above < target && above + scaled >= target) {
-      atomicMin(&L.word[1], static_cast<uint32_t>(tid));
-    }
-    __syncthreads();
-    const uint32_t border = L.word[1];
-    if (border == 0xffffffffu) return false;  // below the bins
-    if (static_cast<uint32_t>(tid) == border) L.word[2] = cnt, L.word[3] = cnt_above, L.value[0] = above;
-    __syncthreads();
-    const uint32_t in_border = L.word[2];
-    const uint32_t n_above = L.word[3];
-    const double mass_above = L.value[0];
-    __syncthreads();
-    const double edge_bin = base - static_cast<double>(border);
-    if (n_above + in_border <= kCandidates) {
-      total = whole * exp2_neg((base - t_max) * (1.0 / 16.0));
-      const double lo = edge_bin / c16;
-      const float low = static_cast<float>(lo - 1e-6 * fabs(lo) - 1e-30);
-      bound = max(bound, logit_key(low));
-    } else {
-      // Too many entries are kept to hold them: only the border bin's are
-      // gathered and ordered; the bins above it are kept whole.
-      if (in_border > kCandidates) return false;
-      if (tid == 0) L.word[0] = 0;
-      __syncthreads();
-      constexpr int kPer = RowView<T>::kPer;
-      const int pieces = (view.lead + V + kPer - 1) / kPer;
-      for (int i = tid; i < pieces; i += kRowThreads) {
-        uint32_t key[kPer];
-        view.piece(P.dbg, i, key);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          if (key[j] <= kMaskedKey) continue;
-          if (floor(static_cast<double>(key_logit(key[j])) * c16) == edge_bin) {
-            const uint32_t n = atomicAdd(&L.word[0], 1u);
-            if (n < kCandidates)
-              L.entry[n] = (static_cast<uint64_t>(key[j]) << 32) |
-                           (0xffffffffu - static_cast<uint32_t>(i * kPer - view.lead + j));
-          }
-        }
-      }
-      __syncthreads();
-      const int n = static_cast<int>(in_border);
-      sort_descending(L.entry, n);
-      auto weight = [&](uint32_t key) {  // relative to 2^(base / 16)
-        const double t = static_cast<double>(key_logit(key)) * c16 - base;
-        return t > 0.0 ? 1.0 / exp2_neg(-t * (1.0 / 16.0)) : exp2_neg(t * (1.0 / 16.0));
-      };
-      // the last kept entry of the bin: the last before which less than the target lies
-      if (tid == 0) L.word[0] = 0;
-      double run = mass_above;
-      for (int i0 = 0; i0 < n; i0 += kRowThreads) {
-        const int i = i0 + tid;
-        const double w = i < n ? weight(static_cast<uint32_t>(L.entry[i] >> 32)) : 0.0;
-        double sum;
-        const double before = run + block_scan_f64(w, L.wave_f64, sum);
-        if (i < n && before < target) atomicMax(&L.word[0], static_cast<uint32_t>(i));
-        run += sum;
-      }
-      __syncthreads();
-      const int last = static_cast<int>(L.word[0]);
-      const uint64_t edge = L.entry[last];
-      const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
-      const int edge_pos = static_cast<int>(0xffffffffu - static_cast<uint32_t>(edge));
-      // each chunk's kept mass: its bins above the border, and its kept entries of the border bin
-      for (int ch = wave; ch < P.chunks; ch += kRowWaves) {
-        const uint32_t ck = dload(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot + ch);
-        double s = 0.0;
-        if (ck > kMaskedKey) {
-          const double off = base - floor(static_cast<double>(key_logit(ck)) * c16);
-          for (int d = lane; d < kScanBins && off + d < border; d += 64) {
-            const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + d);
-            if (w) s += hist_mass(w) * exp2_neg(-(off + d) * (1.0 / 16.0));
-          }
-          for (int i = lane; i <= last; i += 64) {
-            const uint64_t en = L.entry[i];
-            const int e = static_cast<int>(0xffffffffu - static_cast<uint32_t>(en)) + view.lead;
-            if (e / P.chunk_elems == ch) s += weight(static_cast<uint32_t>(en >> 32));
-          }
-        }
-        s = wave_sum_f64(s);
-        if (lane == 0) L.chunk[ch] = s;
-      }
-      __syncthreads();
-      double kept = 0.0, before, w;
-      for (int i = 0; i < P.chunks; ++i) kept += L.chunk[i];
-      const double goal = S.u * kept;
-      const int chunk = find_chunk(L, P.chunks, goal, before);
-      const int at = draw_in_chunk(P, view, L, chunk, before, goal,
-                                   [&](uint32_t key, int pos) {
-                                     const bool in = key > edge_key || (key == edge_key && pos <= edge_pos);
-                                     return in ? weight(key) : 0.0;
-                                   }, w);
-      if (tid == 0) put_draw(P, row, at, w / kept);
-      return true;
-    }
+    RowHistogram H;
+    if (!row_histogram(P, slot, S, m, L, H)) return false;
+    if (H.above + H.in_border > kWaveCandidates) return pick_flat_row(P, row, S, view, m_key, L, H);
+    whole = H.whole * exp2_f64((H.base - static_cast<double>(m) * H.c16) * (1.0 / 16.0));
+    bound = max(bound, first_key_of_bin(H.base - H.border, H.c16, m_key));
   }
 
   // The groups that reach the bound, in order, and their entries that do: the
@@ -900,66 +1294,87 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     const int g0 = min(tid * per, P.groups), g1 = min(g0 + per, P.groups);
     uint32_t mine = 0;
     for (int g = g0; g < g1; ++g) mine += L.group_max[g] >= bound;
-    uint32_t at = block_scan_u32(mine, L.wave_u32, n_list);
+    uint32_t at = block_scan(mine, L.wave_u32[4], n_list);
     if (n_list > kCandidates) return false;
     for (int g = g0; g < g1; ++g)
       if (L.group_max[g] >= bound) L.list[at++] = static_cast<uint32_t>(g);
   }
   __syncthreads();
-  const int per_wave = (static_cast<int>(n_list) + kRowWaves - 1) / kRowWaves;
-  const int l0 = min(wave * per_wave, static_cast<int>(n_list));
-  const int l1 = min(l0 + per_wave, static_cast<int>(n_list));
+  // a wave reads 64 entries at a time: one group of 64, or four of 16
+  const int shift = P.group_shift;
+  const int steps = ((static_cast<int>(n_list) << shift) + 63) >> 6;
+  const int per_wave = (steps + kRowWaves - 1) / kRowWaves;
+  const int l0 = min(wave * per_wave, steps);
+  const int l1 = min(l0 + per_wave, steps);
+  auto element_of = [&](int l) {  // this lane's element of step l, -1 past the list
+    const int i = (l * 64 + lane) >> shift;
+    return i < static_cast<int>(n_list) ? static_cast<int>(L.list[i] << shift) + (lane & ((1 << shift) - 1)) : -1;
+  };
+  auto key_of = [&](int l) { return view.element(P.dbg, element_of(l)); };
+  constexpr int kBatch = 8;  // steps read before any is used, and held for the second round
+  uint32_t held[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) held[b] = l0 + b < l1 ? key_of(l0 + b) : 0u;
   uint32_t found = 0;
-#pragma unroll 4
-  for (int l = l0; l < l1; ++l) {
-    const uint32_t key = view.element(P.dbg, static_cast<int>(L.list[l]) * kGroup + lane);
-    found += __popcll(__ballot(key >= bound));
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(held[b] >= bound));
+  for (int l = l0 + kBatch; l < l1; ++l) found += __popcll(__ballot(key_of(l) >= bound));
+  if (lane == 0) L.wave_u32[5][wave] = found;
+  __syncthreads();
+  uint32_t put = 0, n_cand = 0;
+#pragma unroll
+  for (int w = 0; w < kRowWaves; ++w) {
+    if (w == wave) put = n_cand;
+    n_cand += L.wave_u32[5][w];
   }
-  uint32_t n_cand;
-  uint32_t put = block_scan_u32(lane == 0 ? found : 0u, L.wave_u32, n_cand);
   if (n_cand > kCandidates) return false;
-  put = __shfl(static_cast<int>(put), 0, 64);
-#pragma unroll 4
-  for (int l = l0; l < l1; ++l) {
-    const int e = static_cast<int>(L.list[l]) * kGroup + lane;
-    const uint32_t key = view.element(P.dbg, e);
+  auto keep = [&](uint32_t key, int l) {
     const uint64_t hit = __ballot(key >= bound);
-    const uint32_t at = put + __popcll(hit & ((uint64_t(1) << lane) - 1));
     if (key >= bound) {
+      const uint32_t at = put + __popcll(hit & ((uint64_t(1) << lane) - 1));
       L.cand.key[at] = key;
-      L.cand.pos[at] = e - view.lead;
+      L.cand.pos[at] = element_of(l) - view.lead;
     }
     put += __popcll(hit);
-  }
+  };
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b)
+    if (l0 + b < l1) keep(held[b], l0 + b);
+  for (int l = l0 + kBatch; l < l1; ++l) keep(key_of(l), l);
   __syncthreads();
   const int n = static_cast<int>(n_cand);
+  if (n <= kWaveCandidates) {  // one wave settles them without a barrier
+    if (wave > 0) return true;
+    if (n <= 128) settle_candidates<2>(P, row, S, m, m_key, L, n, whole);
+    else if (n <= 512) settle_candidates<8>(P, row, S, m, m_key, L, n, whole);
+    else settle_candidates<16>(P, row, S, m, m_key, L, n, whole);
+    return true;
+  }
   for (int i = tid; i < n; i += kRowThreads) L.sorted[i] = L.cand.key[i];
   sort_descending(L.sorted, n);
   // the kept prefix of the sorted candidates
   const int kk = static_cast<int>(min(S.k, static_cast<uint32_t>(n)));
   auto weight = [&](uint32_t key) { return weight_of(key, m, m_key, S.c); };
-  double mass = total;
-  if (S.p < 1.0 && S.k < static_cast<uint32_t>(V)) {
+  if (whole < 0.0) {
     double s = 0.0;
     for (int i = tid; i < kk; i += kRowThreads) s += weight(L.sorted[i]);
-    block_scan_f64(s, L.wave_f64, mass);
+    block_scan(s, L.wave_f64[2], whole);
   }
-  const double target = S.p * mass;
-  if (tid == 0) L.word[0] = 0;
+  const double target = S.p * whole;
+  if (tid == 0) L.word[0] = 0, L.word[1] = 0, L.word[2] = 0xffffffffu, L.word[3] = 0;
   double run = 0.0;
   for (int i0 = 0; i0 < kk; i0 += kRowThreads) {
     const int i = i0 + tid;
     const double w = i < kk ? weight(L.sorted[i]) : 0.0;
     double sum;
-    const double before = run + block_scan_f64(w, L.wave_f64, sum);
+    __syncthreads();
+    const double before = run + block_scan(w, L.wave_f64[3], sum);
     if (i < kk && (S.p >= 1.0 || before < target) && w >= S.q) atomicMax(&L.word[0], static_cast<uint32_t>(i));
     run += sum;
   }
   __syncthreads();
   const int last = static_cast<int>(L.word[0]);
   const uint32_t edge = L.sorted[last];
-  if (tid == 0) L.word[1] = 0;
-  __syncthreads();
   for (int i = tid; i <= last; i += kRowThreads)
     if (L.sorted[i] == edge) atomicAdd(&L.word[1], 1u);
   __syncthreads();
@@ -969,21 +1384,18 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   const int c0 = min(tid * per, n), c1 = min(c0 + per, n);
   uint32_t ties = 0, all_ties;
   for (int i = c0; i < c1; ++i) ties += L.cand.key[i] == edge;
-  const uint32_t ties_before = block_scan_u32(ties, L.wave_u32, all_ties);
+  const uint32_t ties_before = block_scan(ties, L.wave_u32[0], all_ties);
   auto kept = [&](int i, uint32_t& t) {
     const uint32_t key = L.cand.key[i];
     if (key < edge) return 0.0;
     if (key == edge && t++ >= quota) return 0.0;
     return weight(key);
   };
-  double sum = 0.0, whole;
+  double sum = 0.0, total;
   uint32_t t = ties_before;
   for (int i = c0; i < c1; ++i) sum += kept(i, t);
-  const double before = block_scan_f64(sum, L.wave_f64, whole);
-  const double goal = S.u * whole;
-  if (tid == 0) L.word[2] = 0xffffffffu, L.word[3] = 0;
-  __syncthreads();
-  double acc = before;
+  double acc = block_scan(sum, L.wave_f64[4], total);
+  const double goal = S.u * total;
   t = ties_before;
   for (int i = c0; i < c1; ++i) {
     const double w = kept(i, t);
@@ -996,7 +1408,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   __syncthreads();
   if (tid == 0) {
     const uint32_t i = L.word[2] != 0xffffffffu ? L.word[2] : L.word[3];
-    put_draw(P, row, L.cand.pos[i], weight(L.cand.key[i]) / whole);
+    put_draw(P, row, L.cand.pos[i], weight(L.cand.key[i]) / total);
   }
   return true;
 }
@@ -1011,8 +1423,6 @@ __global__ __launch_bounds__(kRowThreads) void k_sample_pick(SampleParams P, int
   } lds;
   PickLds& L = lds.pick;
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = tid >> 6;
   const int64_t row = P.row0 + blockIdx.x;
   uint32_t m_key = 0;
   for (int g = tid; g < P.groups; g += kRowThreads) {
@@ -1022,13 +1432,12 @@ __global__ __launch_bounds__(kRowThreads) void k_sample_pick(SampleParams P, int
   }
   const RowSettings S = row_settings(P, row);
   const RowView<T> view(P, row);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m_key = max(m_key, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m_key), o, 64)));
-  if (lane == 0) L.wave_u32[wave] = m_key;
+  m_key = wave_max_u32(m_key);
+  if ((tid & 63) == 0) L.wave_u32[0][tid >> 6] = m_key;
+  if (tid < 16) L.sixteenth[tid] = exp2_f64(tid * (1.0 / 16.0));
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) m_key = max(m_key, L.wave_u32[w]);
-  __syncthreads();
+  for (int w = 0; w < kRowWaves; ++w) m_key = max(m_key, L.wave_u32[0][w]);
   if (!S.valid || m_key <= kMaskedKey) {
     if (tid == 0) put_none(P, row);
     return;
@@ -1065,11 +1474,22 @@ template <class T>
 static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hipStream_t st) {
   // grid x block stays below 2^32 threads
   const int64_t per_row = p.route == kSampleScan ? p.chunks : 1;
+  const int regs = static_cast<int>(ceil_div(p.V, 64));  // a short row's entries per lane
   const int64_t rows_max = std::max<int64_t>(1, (int64_t(1) << 21) / per_row);
   const double bytes = static_cast<double>(p.N) * p.V * sizeof(T);
   for (int64_t r = 0; r < p.N; r += rows_max) {
     const int64_t rows = std::min(p.N - r, rows_max);
     P.row0 = r;
+    if (p.route == kSampleShort) {
+      auto* k = regs <= 1   ? k_sample_short<T, 1>
+                : regs <= 2 ? k_sample_short<T, 2>
+                : regs <= 4 ? k_sample_short<T, 4>
+                : regs <= 8 ? k_sample_short<T, 8>
+                            : k_sample_short<T, 16>;
+      TraceScope ts(st, "sample_short", 0.0, bytes);
+      hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, st, P, rows);
+      continue;
+    }
     if (p.route == kSampleLong) {
       TraceScope ts(st, "sample_long", 0.0, bytes);
       hipLaunchKernelGGL(k_sample_long<T>, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st, P, shift);
@@ -1096,6 +1516,7 @@ hipError_t launch_sample(const SamplePlan& p, const SampleArgs& a, hipStream_t s
   P.token = a.token, P.logprob = a.logprob;
   P.V = static_cast<int32_t>(p.V);
   P.groups = static_cast<int32_t>(p.groups);
+  P.group_shift = p.group_shift;
   P.chunks = static_cast<int32_t>(p.chunks);
   P.chunk_elems = static_cast<int32_t>(p.chunk_elems);
   P.group_max = reinterpret_cast<uint32_t*>(a.ws + p.off_group_max);
