@@ -56,12 +56,21 @@ __device__ __forceinline__ double dpp(double v) {
   return __builtin_bit_cast(double, u32x2{dpp<CTRL, ROWS>(w[0]), dpp<CTRL, ROWS>(w[1])});
 }
 
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint64_t dpp(uint64_t v) {
+  return __builtin_bit_cast(uint64_t, dpp<CTRL, ROWS>(__builtin_bit_cast(double, v)));
+}
+
 __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
   return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
 }
 __device__ __forceinline__ double from_lane(double v, int lane) {
   const u32x2 w = __builtin_bit_cast(u32x2, v);
   return __builtin_bit_cast(double, u32x2{from_lane(w[0], lane), from_lane(w[1], lane)});
+}
+
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int lane) {
+  return __builtin_bit_cast(uint64_t, from_lane(__builtin_bit_cast(double, v), lane));
 }
 
 // Inclusive running sums over the wave: within each row of 16 lanes by shifts
@@ -162,7 +171,8 @@ struct Sixteenths {
 constexpr int kScanElems = 16;             // elements per thread of a scan workgroup
 constexpr int kScanBins = 512;             // mass histogram: bins of 1/16 bit below the chunk's maximum
 constexpr int kCandidates = 4096;          // entries that k_sample_pick settles in LDS,
-constexpr int kWaveCandidates = 1024;       // and how many of them by one wave
+constexpr int kWaveCandidates = 128;       // and how many of them by one wave
+constexpr int kFlatRow = 1024;             // kept entries above which only the border's are gathered
 constexpr int kShortRow = 1024;
 
 struct SampleParams {
@@ -216,11 +226,12 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& P, int64
 
 // What the scan leaves for a row beside the maxima: nothing where top-k or
 // min-p bound the border by themselves, each chunk's mass where the whole
-// row's mass counts, each chunk's mass histogram where top-p alone decides.
+// row's mass counts, each chunk's mass histogram where top-p alone decides, or
+// top-k with too many entries for the group maxima to bound it well.
 enum RowMode { kMaximaOnly, kChunkMass, kMassHistogram };
 
-__device__ __forceinline__ RowMode row_mode(const RowSettings& s, int V) {
-  if (s.k < static_cast<uint32_t>(V)) return kMaximaOnly;
+__device__ __forceinline__ RowMode row_mode(const RowSettings& s, const SampleParams& P) {
+  if (s.k < static_cast<uint32_t>(P.V)) return s.k > static_cast<uint32_t>(P.groups) / 4 ? kMassHistogram : kMaximaOnly;
   if (s.p < 1.0) return s.q > 0.0 ? kChunkMass : kMassHistogram;
   return s.q > 0.0 ? kMaximaOnly : kChunkMass;
 }
@@ -468,6 +479,23 @@ struct RowView {
     return v;
   }
 
+  // Pieces i0 + tid + b * stride, b < N, for a block of `stride` threads: all
+  // inside the row but for the first and last such batches, which alone look at
+  // every piece (a load behind a branch of its own waits there).
+  template <int N>
+  __device__ __forceinline__ void batch(const DebugCheck& dbg, int i0, int stride, u32x4 (&v)[N]) const {
+    const int first = i0 + static_cast<int>(threadIdx.x);
+    if (i0 * kPer - lead >= 0 && (i0 + N * stride) * kPer - lead <= V) {
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+        v[b] = dload(dbg, 0, kDbgSampleLogits,
+                     reinterpret_cast<const u32x4*>(x + ((first + b * stride) * kPer - lead)));
+    } else {
+#pragma unroll
+      for (int b = 0; b < N; ++b) v[b] = raw(dbg, first + b * stride);
+    }
+  }
+
   static __device__ __forceinline__ float logit(const u32x4& v, int j) {
     const uint32_t w = v[j * sizeof(T) / 4];
     return logit_of_bits<T>(sizeof(T) == 4 ? w : (j & 1) ? w >> 16 : w & 0xffffu);
@@ -482,7 +510,9 @@ struct RowView {
 
   __device__ __forceinline__ uint32_t element(const DebugCheck& dbg, int e) const {
     const int at = e - lead;  // before the row for a negative e
-    return at >= 0 && at < V ? logit_key(static_cast<float>(dload(dbg, 0, kDbgSampleLogits, x + at))) : 0u;
+    const int in = min(max(at, 0), V - 1);  // read in any case: no branch to wait in
+    const uint32_t key = logit_key(static_cast<float>(dload(dbg, 0, kDbgSampleLogits, x + in)));
+    return at == in ? key : 0u;
   }
 };
 
@@ -531,11 +561,15 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   const int64_t row = P.row0 + blockIdx.x / P.chunks;
   const RowView<T> view(P, row);
   const int64_t slot = row * P.chunks + chunk;
+  u32x4 held[kPieces];
+  view.template batch<kPieces>(P.dbg, chunk * (kThreads * kPieces), kThreads, held);
   float x[kPieces][kPer];
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) view.logits(P.dbg, chunk * (kThreads * kPieces) + p * kThreads + tid, x[p]);
+  for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[p][j] = view.logit(held[p], j);
   const RowSettings S = row_settings(P, row);
-  const RowMode mode = row_mode(S, P.V);
+  const RowMode mode = row_mode(S, P);
   float top = -INFINITY;
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
@@ -638,10 +672,12 @@ struct PickLds {
     } half;  // the second half of the block's sums over the chunks
   };
   union {
-    uint32_t sorted[kCandidates];
     uint32_t bins[kRowThreads];
     uint32_t list[kCandidates];  // groups that reach the bound
-    uint64_t sub[kRowThreads];   // the border bin's finer histogram
+    struct {  // finer histogram of the entries among which the border lies
+      uint32_t count[kRowThreads];
+      uint64_t units[kRowThreads];
+    } fine;
   };
   double bin_scale[kScanBins];  // 2^(-d / 16)
   double sixteenth[16];         // 2^(j / 16)
@@ -649,48 +685,46 @@ struct PickLds {
   uint64_t chunk_units[kMaxChunks];
   int32_t chunk_off[kMaxChunks];
   double wave_f64[6][kRowWaves];
+  uint64_t wave_u64[kRowWaves];
   uint32_t wave_u32[6][kRowWaves];
   uint32_t word[10];
-  double value[2];
+  double value;
+  uint64_t units;
   uint64_t edge;
   uint32_t few[64];
 };
 
 // Exclusive sum of v over the block in thread order; total gets the sum. One
-// barrier: `wave` must not have been in use since the last one.
+// barrier: `wave` must not have been in use since the last one. Every wave adds
+// up the 16 waves' sums in a row of its lanes.
 template <class V>
 __device__ __forceinline__ V block_scan(V v, V* wave, V& total) {
+  static_assert(kRowWaves == 16, "one row of lanes");
   const V incl = wave_scan(v);
-  if ((threadIdx.x & 63) == 63) wave[threadIdx.x >> 6] = incl;
+  const int lane = threadIdx.x & 63;
+  if (lane == 63) wave[threadIdx.x >> 6] = incl;
   __syncthreads();
-  V base = 0, sum = 0;
-#pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) {
-    if (w == static_cast<int>(threadIdx.x >> 6)) base = sum;
-    sum += wave[w];
-  }
-  total = sum;
+  V w = wave[lane & 15];
+  w += dpp<0x111>(w);
+  w += dpp<0x112>(w);
+  w += dpp<0x114>(w);
+  w += dpp<0x118>(w);
+  total = from_lane(w, 15);
+  const int me = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const V base = me > 0 ? from_lane(w, me - 1) : V(0);
   return base + (incl - v);
 }
 
-// Sorts n keys (LDS, room for the next power of two >= 64) in descending order;
-// the keys past n are 0.
-__device__ void sort_descending(uint32_t* a, int n) {
-  int size = 64;
-  while (size < n) size <<= 1;
-  const int tid = threadIdx.x;
-  for (int i = n + tid; i < size; i += kRowThreads) a[i] = 0;
-  __syncthreads();
-  for (int k = 2; k <= size; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int p = tid; p < size / 2; p += kRowThreads) {
-        const int i = 2 * p - (p & (j - 1));
-        const uint32_t x = a[i], y = a[i + j];
-        if ((x < y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
-      }
-      __syncthreads();
-    }
-  }
+// Least and largest index of the block at which `hit`, whose lanes' indices
+// rise with the lane: one atomic per wave, since those of many lanes on one
+// address are carried out one after the other.
+__device__ __forceinline__ void put_first(uint32_t* word, bool hit, uint32_t index) {
+  const uint64_t b = __ballot(hit);
+  if (b && (threadIdx.x & 63) == static_cast<uint32_t>(__ffsll(static_cast<long long>(b)) - 1)) atomicMin(word, index);
+}
+__device__ __forceinline__ void put_last(uint32_t* word, bool hit, uint32_t index) {
+  const uint64_t b = __ballot(hit);
+  if (b && (threadIdx.x & 63) == static_cast<uint32_t>(63 - __clzll(static_cast<long long>(b)))) atomicMax(word, index);
 }
 
 // One compare-exchange step of a wave's bitonic sort (descending) of 64 R keys,
@@ -930,15 +964,13 @@ __device__ __forceinline__ void draw_in_chunk(const SampleParams& P, int64_t row
     }
     __syncthreads();
     double run = base + block_scan(sum, L.wave_f64[5], total);
-    if (sum > 0.0) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        run += w[j];
-        if (first_at < 0 && w[j] > 0.0 && run > goal) first_at = pos + j, first_w = w[j];
-      }
-      if (first_at >= 0) atomicMin(&L.word[0], static_cast<uint32_t>(first_at));
-      atomicMax(&L.word[1], static_cast<uint32_t>(last_at));
+    for (int j = 0; j < kPer; ++j) {
+      run += w[j];
+      if (first_at < 0 && w[j] > 0.0 && run > goal) first_at = pos + j, first_w = w[j];
     }
+    put_first(&L.word[0], first_at >= 0, static_cast<uint32_t>(first_at));
+    put_last(&L.word[1], sum > 0.0, static_cast<uint32_t>(last_at));
     base += total;
     __syncthreads();
     if (L.word[0] != 0xffffffffu) break;
@@ -970,7 +1002,7 @@ __device__ __forceinline__ int find_chunk(const PickLds& L, int n, double u, dou
 struct RowHistogram {
   double c16, base;   // the grid, and the bin of the row's largest logit
   double whole;       // the row's mass relative to 2^(base / 16)
-  uint32_t border;    // the bin (from the top) in which the mass reaches target
+  uint32_t border;    // the bin (from the top) in which the mass reaches target, or the count top-k
   uint32_t in_border, above;  // entries in it and above it
   double mass_above;
   double target;
@@ -1000,15 +1032,28 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
   const int bin = tid % kScanBins;
   uint32_t count = 0;
   double mass = 0.0;
-#pragma unroll 4
-  for (int ch = tid / kScanBins; ch < P.chunks; ch += kRowThreads / kScanBins) {
-    const int off = L.chunk_off[ch];
-    const bool inside = off <= bin;  // otherwise a chunk bin below the row's last
-    const int i = off >= kScanBins ? bin : inside ? bin - off : bin - off + kScanBins;
-    const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + i);
-    const double v = units_mass(hist_units(w));
-    if (inside) count += hist_count(w), mass += v;
-    else if (w) rest += v * power(L, -(off + i));
+  constexpr int kBatch = 8;  // words read before any is used
+  for (int c0 = tid / kScanBins; c0 < P.chunks; c0 += kBatch * (kRowThreads / kScanBins)) {
+    uint64_t w[kBatch];
+    int off[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int ch = c0 + b * (kRowThreads / kScanBins);
+      w[b] = 0;
+      if (ch < P.chunks) {
+        off[b] = L.chunk_off[ch];
+        // row bin `bin` where the chunk has it, otherwise the chunk bin that lies below the row's last
+        const int i = off[b] >= kScanBins ? bin : (bin - off[b]) & (kScanBins - 1);
+        w[b] = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + i);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (w[b] == 0) continue;
+      const double v = units_mass(hist_units(w[b]));
+      if (off[b] <= bin) count += hist_count(w[b]), mass += v;
+      else rest += v * power(L, -(off[b] >= kScanBins ? off[b] + bin : bin + kScanBins));
+    }
   }
   if (tid >= kScanBins) L.half.count[bin] = count, L.half.mass[bin] = mass;
   __syncthreads();
@@ -1022,157 +1067,123 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
   const uint32_t count_above = block_scan(count, L.wave_u32[2], counted);
   H.whole = in_bins + rest_all;
   H.target = S.p * H.whole;
-  if (count > 0 && above < H.target && above + scaled >= H.target) atomicMin(&L.word[2], static_cast<uint32_t>(tid));
+  const bool here = S.k < static_cast<uint32_t>(P.V) ? count_above < S.k && count_above + count >= S.k
+                                                     : above < H.target && above + scaled >= H.target;
+  put_first(&L.word[2], count > 0 && here, static_cast<uint32_t>(tid));
   __syncthreads();
   H.border = L.word[2];
   if (H.border == 0xffffffffu) return false;
-  if (static_cast<uint32_t>(tid) == H.border) L.word[3] = count, L.word[4] = count_above, L.value[0] = above;
+  if (static_cast<uint32_t>(tid) == H.border) L.word[3] = count, L.word[4] = count_above, L.value = above;
   __syncthreads();
   H.in_border = L.word[3];
   H.above = L.word[4];
-  H.mass_above = L.value[0];
+  H.mass_above = L.value;
   return true;
 }
 
-// A row of which top-p keeps more entries than one wave settles: the
-// bins above the border are kept whole, and only the border bin's entries are
-// gathered (one read of the row), counted into 1024 finer bins, and settled
-// there: a few entries by comparing them all, many equal ones by their
-// positions. false where neither is the case.
-template <class T>
-__device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row, const RowSettings& S,
-                                              const RowView<T>& view, uint32_t m_key, PickLds& L,
-                                              const RowHistogram& H) {
+// The last entry kept of a list in LDS: the last, in the order of (key
+// descending, position ascending), before which the entries of keys in [lo,
+// hi) amount to less than `target`: their number, or the units of their
+// weights. entry(i) = (key, ~position), 0 <= i < n, so that larger values come
+// first; at least one entry has a key in [lo, hi) and target > 0. The keys are
+// counted into 1024 bins, then those of the bin at which the target is reached
+// again, until that bin holds at most 64 entries, which one wave compares, or
+// entries of one key, of which the last one's position is looked for among
+// 1024 bins of positions. Returns the entry to every thread.
+template <class Entry, class Units>
+__device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint32_t lo, uint64_t hi, bool by_units,
+                                                 uint64_t target, Entry entry, Units units) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int wave = tid >> 6;
-  const int V = P.V;
-  const int64_t slot = row * P.chunks;
-  if (H.in_border > kCandidates) return false;
-  const int n = static_cast<int>(H.in_border);
-  const double edge_bin = H.base - H.border;
-  if (wave < 2) {
-    const uint32_t key = first_key_of_bin(edge_bin + wave, H.c16, m_key);
-    if (lane == 0) L.word[wave] = key;
-  }
-  __syncthreads();
-  const uint32_t k_lo = L.word[0], k_hi = L.word[1];
-  const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
-  const int sub_shift = max(0, 22 - __clz(static_cast<int>((k_hi - k_lo - 1) | 1)));
-  auto units = [&](uint32_t key) {
-    return hist_units(hist_word(Sixteenths(static_cast<double>(key_logit(key)) * H.c16)));
-  };
-  const double scale = L.bin_scale[H.border] * (1.0 / (uint64_t(1) << kHistShift));  // of the border bin's units
-  __syncthreads();
-  L.sub[tid] = 0;
-  if (tid < P.chunks) L.chunk_units[tid] = 0;
-  if (tid == 0) L.word[0] = 0, L.word[5] = 0, L.word[6] = 0, L.word[7] = 0xffffffffu, L.word[8] = 0;
-  __syncthreads();
-  constexpr int kPer = RowView<T>::kPer;
-  const int pieces = (view.lead + V + kPer - 1) / kPer;
-  auto take = [&](float x, int pos) {
-    const uint32_t key = logit_key(x);
-    const uint32_t at = atomicAdd(&L.word[0], 1u);
-    if (at < kCandidates) L.entry[at] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(pos));
-    atomicAdd(reinterpret_cast<unsigned long long*>(&L.sub[min((key - k_lo) >> sub_shift, 1023u)]),
-              static_cast<unsigned long long>((uint64_t(1) << kHistCount) + units(key)));
-  };
-  constexpr int kBatch = 4;  // pieces read before any is looked at
-  for (int i0 = tid; i0 < pieces; i0 += kBatch * kRowThreads) {
-    u32x4 held[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) held[b] = view.raw(P.dbg, i0 + b * kRowThreads);  // -inf past the row
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      uint32_t hits = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float x = view.logit(held[b], j);
-        hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << j;
-      }
-      if (hits) {
-        const int pos = (i0 + b * kRowThreads) * kPer - view.lead;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (hits >> j & 1) take(view.logit(held[b], j), pos + j);
-      }
-    }
-  }
-  __syncthreads();
-  // the finer bin at which the mass reaches the target (the last one if rounding leaves none)
-  const uint64_t word = L.sub[kRowThreads - 1 - tid];
-  const uint32_t count = hist_count(word);
-  const double mass = static_cast<double>(hist_units(word)) * scale;
-  double sum;
-  const double above = H.mass_above + block_scan(mass, L.wave_f64[2], sum);
-  if (count > 0 && (above < H.target || tid == 0)) atomicMax(&L.word[5], static_cast<uint32_t>(tid));
-  __syncthreads();
-  const uint32_t sub = kRowThreads - 1 - L.word[5];
-  if (static_cast<uint32_t>(tid) == L.word[5]) L.word[9] = count, L.value[1] = above;
-  __syncthreads();
-  const int n_sub = static_cast<int>(L.word[9]);
-  const double above_sub = L.value[1];
-  if (n_sub <= 64) {
-    for (int i = tid; i < n; i += kRowThreads)
-      if (min((static_cast<uint32_t>(L.entry[i] >> 32) - k_lo) >> sub_shift, 1023u) == sub)
-        L.few[atomicAdd(&L.word[6], 1u)] = static_cast<uint32_t>(i);
+  uint64_t above = 0;
+  int count;
+  for (;;) {
+    const uint32_t span = static_cast<uint32_t>(hi - lo - 1);
+    const int shift = max(0, 22 - __clz(static_cast<int>(span | 1)));
     __syncthreads();
-    if (wave == 0) {
-      const uint64_t mine = lane < n_sub ? L.entry[L.few[lane]] : 0;
-      uint64_t before = 0;
-      uint64_t edge = ~uint64_t(0);
-      for (int i = 0; i < n_sub; ++i) {
-        const uint64_t other = (static_cast<uint64_t>(from_lane(static_cast<uint32_t>(mine >> 32), i)) << 32) |
-                               from_lane(static_cast<uint32_t>(mine), i);
-        if (other > mine) before += units(static_cast<uint32_t>(other >> 32));
-      }
-      const bool keep = lane < n_sub && (before == 0 || above_sub + static_cast<double>(before) * scale < H.target);
-      for (uint64_t left = __ballot(keep); left; left &= left - 1) {
-        const int i = __ffsll(static_cast<long long>(left)) - 1;
-        const uint64_t other = (static_cast<uint64_t>(from_lane(static_cast<uint32_t>(mine >> 32), i)) << 32) |
-                               from_lane(static_cast<uint32_t>(mine), i);
-        edge = min(edge, other);
-      }
-      if (lane == 0) L.edge = edge;
+    L.fine.count[tid] = 0;
+    L.fine.units[tid] = 0;
+    if (tid == 0) L.word[5] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint32_t key = static_cast<uint32_t>(entry(i) >> 32);
+      if (key < lo || key >= hi) continue;
+      // 16-bit logits come in few values: lanes of the first lane's key are counted at once
+      const uint32_t lead = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(key)));
+      const uint64_t same = __ballot(key == lead);
+      const uint32_t times = key != lead ? 1u : lane == __ffsll(static_cast<long long>(same)) - 1 ? __popcll(same) : 0u;
+      if (times == 0) continue;
+      atomicAdd(&L.fine.count[(key - lo) >> shift], times);
+      if (by_units)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&L.fine.units[(key - lo) >> shift]),
+                  static_cast<unsigned long long>(units(key) * times));
+    }
+    __syncthreads();
+    const int bin = kRowThreads - 1 - tid;
+    const uint32_t here = L.fine.count[bin];
+    uint64_t sum;
+    const uint64_t before = above + block_scan(by_units ? L.fine.units[bin] : uint64_t(here), L.wave_u64, sum);
+    put_last(&L.word[5], here > 0 && before < target, static_cast<uint32_t>(tid));
+    __syncthreads();
+    const int at = static_cast<int>(L.word[5]);
+    if (tid == at) L.word[6] = here, L.units = before;
+    __syncthreads();
+    count = static_cast<int>(L.word[6]);
+    above = L.units;
+    lo += static_cast<uint32_t>(kRowThreads - 1 - at) << shift;
+    hi = min(hi, static_cast<uint64_t>(lo) + (uint64_t(1) << shift));
+    if (count <= 64 || shift == 0) break;
+  }
+  L.few[lane] = 0;
+  if (tid == 0) L.word[7] = 0;
+  __syncthreads();
+  if (count <= 64) {
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint32_t key = static_cast<uint32_t>(entry(i) >> 32);
+      if (key >= lo && key < hi) L.few[atomicAdd(&L.word[7], 1u)] = static_cast<uint32_t>(i);
+    }
+    __syncthreads();
+    if (tid < 64) {
+      const uint64_t mine = lane < count ? entry(static_cast<int>(L.few[lane])) : 0;
+      const uint64_t w = by_units ? units(static_cast<uint32_t>(mine >> 32)) : 1;
+      uint64_t before = above;
+      for (int i = 0; i < count; ++i)
+        if (from_lane(mine, i) > mine) before += from_lane(w, i);
+      uint64_t last = ~uint64_t(0);  // of those kept; the first one is, above < target
+      for (uint64_t left = __ballot(lane < count && before < target); left; left &= left - 1)
+        last = min(last, from_lane(mine, __ffsll(static_cast<long long>(left)) - 1));
+      if (lane == 0) L.edge = last;
     }
   } else {
-    // many entries: settled only if they are all equal
-    for (int i = tid; i < n; i += kRowThreads) {
-      const uint32_t key = static_cast<uint32_t>(L.entry[i] >> 32);
-      if (min((key - k_lo) >> sub_shift, 1023u) == sub) atomicMin(&L.word[7], key), atomicMax(&L.word[8], key);
-    }
-    L.few[lane] = 0;
-    __syncthreads();
-    const uint32_t key = L.word[7];
-    if (key != L.word[8]) return false;
-    const double each = static_cast<double>(units(key)) * scale;
-    const double want = ceil((H.target - above_sub) / each);
-    const uint32_t quota = want < 1.0 ? 1u : want > n_sub ? static_cast<uint32_t>(n_sub) : static_cast<uint32_t>(want);
-    // the quota-th of their positions: by bins of 2^pos_shift positions, then a bitmap of the bin
+    const uint64_t each = by_units ? max(units(lo), uint64_t(1)) : 1;
+    const uint64_t want = (target - above + each - 1) / each;  // >= 1
+    const uint32_t quota = static_cast<uint32_t>(min(want, static_cast<uint64_t>(count)));
     int pos_shift = 0;
     while ((V - 1) >> pos_shift >= kRowThreads) ++pos_shift;
     L.bins[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kRowThreads)
-      if (static_cast<uint32_t>(L.entry[i] >> 32) == key)
-        atomicAdd(&L.bins[(0xffffffffu - static_cast<uint32_t>(L.entry[i])) >> pos_shift], 1u);
+    for (int i = tid; i < n; i += kRowThreads) {
+      const uint64_t e = entry(i);
+      if (static_cast<uint32_t>(e >> 32) == lo) atomicAdd(&L.bins[~static_cast<uint32_t>(e) >> pos_shift], 1u);
+    }
     __syncthreads();
     const uint32_t here = L.bins[tid];
     uint32_t all;
     const uint32_t before = block_scan(here, L.wave_u32[3], all);
-    if (before < quota && before + here >= quota) L.word[3] = static_cast<uint32_t>(tid), L.word[4] = quota - before;
+    if (before < quota && before + here >= quota) L.word[8] = static_cast<uint32_t>(tid), L.word[9] = quota - before;
     __syncthreads();
-    const uint32_t pos_bin = L.word[3];
+    const uint32_t pos_bin = L.word[8];
     for (int i = tid; i < n; i += kRowThreads) {
-      const uint32_t pos = 0xffffffffu - static_cast<uint32_t>(L.entry[i]);
-      if (static_cast<uint32_t>(L.entry[i] >> 32) == key && pos >> pos_shift == pos_bin) {
-        const uint32_t bit = pos & ((1u << pos_shift) - 1);
+      const uint64_t e = entry(i);
+      const uint32_t pos = ~static_cast<uint32_t>(e);
+      if (static_cast<uint32_t>(e >> 32) == lo && pos >> pos_shift == pos_bin) {
+        const uint32_t bit = pos & ((1u << pos_shift) - 1);  // below 256
         atomicOr(&L.few[bit >> 5], 1u << (bit & 31));
       }
     }
     __syncthreads();
     if (tid == 0) {
-      uint32_t nth = L.word[4], pos = pos_bin << pos_shift;
+      uint32_t nth = L.word[9], pos = pos_bin << pos_shift;
       for (int i = 0; i < 8; ++i) {
         uint32_t bits = L.few[i];
         const uint32_t c = static_cast<uint32_t>(__popc(bits));
@@ -1184,18 +1195,85 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
         pos += static_cast<uint32_t>(i * 32 + __ffs(static_cast<int>(bits)) - 1);
         break;
       }
-      L.edge = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - pos);
+      L.edge = (static_cast<uint64_t>(lo) << 32) | ~pos;
     }
   }
   __syncthreads();
-  const uint64_t edge = L.edge;
+  return L.edge;
+}
+
+// A row of which more entries are kept than the workgroup holds: the bins
+// above the border are kept whole, and only the border bin's entries are
+// gathered (one read of the row) and settled. false where they are too many.
+template <class T>
+__device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row, const RowSettings& S,
+                                              const RowView<T>& view, uint32_t m_key, PickLds& L,
+                                              const RowHistogram& H) {
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = tid >> 6;
+  const int V = P.V;
+  const int64_t slot = row * P.chunks;
+  const bool by_count = S.k < static_cast<uint32_t>(V);
+  if (H.in_border > kCandidates || (by_count && (S.p < 1.0 || S.q > 0.0))) return false;
+  const int n = static_cast<int>(H.in_border);
+  const double edge_bin = H.base - H.border;
+  if (wave < 2) {
+    const uint32_t key = first_key_of_bin(edge_bin + wave, H.c16, m_key);
+    if (lane == 0) L.word[wave] = key;
+  }
+  if (tid < P.chunks) L.chunk_units[tid] = 0;
+  if (tid == 0) L.word[2] = 0;
+  __syncthreads();
+  const uint32_t k_lo = L.word[0], k_hi = L.word[1];
+  const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
+  constexpr int kPer = RowView<T>::kPer;
+  const int pieces = (view.lead + V + kPer - 1) / kPer;
+  constexpr int kBatch = 4;  // pieces read before any is looked at
+  uint32_t* const found = L.list;  // positions
+  for (int p0 = 0; p0 < pieces; p0 += kBatch * kRowThreads) {  // the same for all lanes: they vote below
+    const int i0 = p0 + tid;
+    u32x4 held[kBatch];
+    view.template batch<kBatch>(P.dbg, p0, kRowThreads, held);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float x = view.logit(held[b], j);
+        hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << j;
+      }
+      if (__ballot(hits != 0) == 0) continue;
+      const uint32_t mine = static_cast<uint32_t>(__popc(hits));
+      const uint32_t incl = wave_scan(mine);
+      uint32_t at = 0;
+      if (lane == 63) at = atomicAdd(&L.word[2], incl);
+      at = from_lane(at, 63) + incl - mine;
+      const int pos = (i0 + b * kRowThreads) * kPer - view.lead;
+      for (; hits; hits &= hits - 1, ++at)
+        if (at < kCandidates) found[at] = static_cast<uint32_t>(pos + __ffs(static_cast<int>(hits)) - 1);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kRowThreads) {
+    const uint32_t pos = found[i];
+    const uint32_t key = view.element(P.dbg, static_cast<int>(pos) + view.lead);
+    L.entry[i] = (static_cast<uint64_t>(key) << 32) | ~pos;
+  }
+  auto units = [&](uint32_t key) {
+    return hist_units(hist_word(Sixteenths(static_cast<double>(key_logit(key)) * H.c16)));
+  };
+  const double scale = L.bin_scale[H.border] * (1.0 / (uint64_t(1) << kHistShift));  // of the border bin's units
+  const double want = ceil((H.target - H.mass_above) / scale);
+  const uint64_t target = by_count ? S.k - H.above : want < 1.0 ? 1 : static_cast<uint64_t>(want);
+  const uint64_t edge = border_entry(L, V, n, k_lo, k_hi, !by_count, target, [&](int i) { return L.entry[i]; }, units);
   const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
-  const int edge_pos = static_cast<int>(0xffffffffu - static_cast<uint32_t>(edge));
+  const int edge_pos = static_cast<int>(~static_cast<uint32_t>(edge));
   // each chunk's kept mass: its bins above the border, and its kept entries of the border bin
   for (int i = tid; i < n; i += kRowThreads) {
     const uint64_t e = L.entry[i];
     if (e >= edge) {
-      const int at = static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) + view.lead;
+      const int at = static_cast<int>(~static_cast<uint32_t>(e)) + view.lead;
       atomicAdd(reinterpret_cast<unsigned long long*>(&L.chunk_units[at / P.chunk_elems]),
                 static_cast<unsigned long long>(units(static_cast<uint32_t>(e >> 32))));
     }
@@ -1244,7 +1322,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   const int lane = tid & 63;
   const int wave = tid >> 6;
   const int V = P.V;
-  const RowMode mode = row_mode(S, V);
+  const RowMode mode = row_mode(S, P);
   const float m = key_logit(m_key);
   const int64_t slot = row * P.chunks;
   const bool all = S.k >= static_cast<uint32_t>(V);  // top-k is off
@@ -1270,7 +1348,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
 
   // a key that every kept entry reaches
   uint32_t bound = kMaskedKey + 1;
-  if (!all) bound = S.k == 1 ? m_key : bound_of_kth(L, P.groups, m_key, S.k);
+  if (!all && mode == kMaximaOnly) bound = S.k == 1 ? m_key : bound_of_kth(L, P.groups, m_key, S.k);
   if (S.q > 0.0 && isfinite(m) && (S.p >= 1.0 || all)) {
     // w >= q: x >= m + log2(q) / c, taken lower by more than its rounding
     // (top-p after top-k needs the mass of all the k entries: no bound from q then)
@@ -1281,8 +1359,9 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   if (mode == kMassHistogram) {
     RowHistogram H;
     if (!row_histogram(P, slot, S, m, L, H)) return false;
-    if (H.above + H.in_border > kWaveCandidates) return pick_flat_row(P, row, S, view, m_key, L, H);
-    whole = H.whole * exp2_f64((H.base - static_cast<double>(m) * H.c16) * (1.0 / 16.0));
+    const bool wide = H.above + H.in_border > (all ? kFlatRow : kCandidates);
+    if (wide && (all || S.p < 1.0 || S.q <= 0.0)) return pick_flat_row(P, row, S, view, m_key, L, H);
+    if (all) whole = H.whole * exp2_f64((H.base - static_cast<double>(m) * H.c16) * (1.0 / 16.0));
     bound = max(bound, first_key_of_bin(H.base - H.border, H.c16, m_key));
   }
 
@@ -1311,14 +1390,26 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     return i < static_cast<int>(n_list) ? static_cast<int>(L.list[i] << shift) + (lane & ((1 << shift) - 1)) : -1;
   };
   auto key_of = [&](int l) { return view.element(P.dbg, element_of(l)); };
-  constexpr int kBatch = 8;  // steps read before any is used, and held for the second round
-  uint32_t held[kBatch];
+  // steps read before any is used; the first batch is held for the second round
+  constexpr int kBatch = 8;
+  uint32_t first[kBatch];
+  auto read = [&](int l, uint32_t (&key)[kBatch]) {
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) held[b] = l0 + b < l1 ? key_of(l0 + b) : 0u;
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t k = key_of(l + b);
+      key[b] = l + b < l1 ? k : 0u;
+    }
+  };
+  read(l0, first);
   uint32_t found = 0;
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(held[b] >= bound));
-  for (int l = l0 + kBatch; l < l1; ++l) found += __popcll(__ballot(key_of(l) >= bound));
+  for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(first[b] >= bound));
+  for (int l = l0 + kBatch; l < l1; l += kBatch) {
+    uint32_t key[kBatch];
+    read(l, key);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(key[b] >= bound));
+  }
   if (lane == 0) L.wave_u32[5][wave] = found;
   __syncthreads();
   uint32_t put = 0, n_cand = 0;
@@ -1328,83 +1419,81 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     n_cand += L.wave_u32[5][w];
   }
   if (n_cand > kCandidates) return false;
-  auto keep = [&](uint32_t key, int l) {
-    const uint64_t hit = __ballot(key >= bound);
-    if (key >= bound) {
-      const uint32_t at = put + __popcll(hit & ((uint64_t(1) << lane) - 1));
-      L.cand.key[at] = key;
-      L.cand.pos[at] = element_of(l) - view.lead;
-    }
-    put += __popcll(hit);
-  };
+  auto keep = [&](int l, const uint32_t (&key)[kBatch]) {
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b)
-    if (l0 + b < l1) keep(held[b], l0 + b);
-  for (int l = l0 + kBatch; l < l1; ++l) keep(key_of(l), l);
+    for (int b = 0; b < kBatch; ++b) {
+      const uint64_t hit = __ballot(key[b] >= bound);
+      if (key[b] >= bound) {
+        const uint32_t at = put + __popcll(hit & ((uint64_t(1) << lane) - 1));
+        L.cand.key[at] = key[b];
+        L.cand.pos[at] = element_of(l + b) - view.lead;
+      }
+      put += __popcll(hit);
+    }
+  };
+  keep(l0, first);
+  for (int l = l0 + kBatch; l < l1; l += kBatch) {
+    uint32_t key[kBatch];
+    read(l, key);
+    keep(l, key);
+  }
   __syncthreads();
   const int n = static_cast<int>(n_cand);
   if (n <= kWaveCandidates) {  // one wave settles them without a barrier
-    if (wave > 0) return true;
-    if (n <= 128) settle_candidates<2>(P, row, S, m, m_key, L, n, whole);
-    else if (n <= 512) settle_candidates<8>(P, row, S, m, m_key, L, n, whole);
-    else settle_candidates<16>(P, row, S, m, m_key, L, n, whole);
+    if (wave == 0) settle_candidates<kWaveCandidates / 64>(P, row, S, m, m_key, L, n, whole);
     return true;
   }
-  for (int i = tid; i < n; i += kRowThreads) L.sorted[i] = L.cand.key[i];
-  sort_descending(L.sorted, n);
-  // the kept prefix of the sorted candidates
-  const int kk = static_cast<int>(min(S.k, static_cast<uint32_t>(n)));
-  auto weight = [&](uint32_t key) { return weight_of(key, m, m_key, S.c); };
-  if (whole < 0.0) {
-    double s = 0.0;
-    for (int i = tid; i < kk; i += kRowThreads) s += weight(L.sorted[i]);
-    block_scan(s, L.wave_f64[2], whole);
-  }
-  const double target = S.p * whole;
-  if (tid == 0) L.word[0] = 0, L.word[1] = 0, L.word[2] = 0xffffffffu, L.word[3] = 0;
-  double run = 0.0;
-  for (int i0 = 0; i0 < kk; i0 += kRowThreads) {
-    const int i = i0 + tid;
-    const double w = i < kk ? weight(L.sorted[i]) : 0.0;
-    double sum;
-    __syncthreads();
-    const double before = run + block_scan(w, L.wave_f64[3], sum);
-    if (i < kk && (S.p >= 1.0 || before < target) && w >= S.q) atomicMax(&L.word[0], static_cast<uint32_t>(i));
-    run += sum;
-  }
-  __syncthreads();
-  const int last = static_cast<int>(L.word[0]);
-  const uint32_t edge = L.sorted[last];
-  for (int i = tid; i <= last; i += kRowThreads)
-    if (L.sorted[i] == edge) atomicAdd(&L.word[1], 1u);
-  __syncthreads();
-  const uint32_t quota = L.word[1];  // of the entries equal to the border's, the first this many positions
-  // the draw: thread t holds candidates t * per .. in order of position
-  const int per = (n + kRowThreads - 1) / kRowThreads;
-  const int c0 = min(tid * per, n), c1 = min(c0 + per, n);
-  uint32_t ties = 0, all_ties;
-  for (int i = c0; i < c1; ++i) ties += L.cand.key[i] == edge;
-  const uint32_t ties_before = block_scan(ties, L.wave_u32[0], all_ties);
-  auto kept = [&](int i, uint32_t& t) {
-    const uint32_t key = L.cand.key[i];
-    if (key < edge) return 0.0;
-    if (key == edge && t++ >= quota) return 0.0;
-    return weight(key);
+  auto weight = [&](uint32_t key) {
+    const float x = key_logit(key);
+    return x == m ? 1.0 : power(L, (static_cast<double>(x) - static_cast<double>(m)) * (16.0 * S.c));
   };
-  double sum = 0.0, total;
-  uint32_t t = ties_before;
-  for (int i = c0; i < c1; ++i) sum += kept(i, t);
-  double acc = block_scan(sum, L.wave_f64[4], total);
+  constexpr double kUnit = static_cast<double>(uint64_t(1) << 46);  // 4096 weights of at most 1 stay below 2^59
+  auto units = [&](uint32_t key) { return static_cast<uint64_t>(weight(key) * kUnit + 0.5); };
+  auto entry = [&](int i) {
+    return (static_cast<uint64_t>(L.cand.key[i]) << 32) | ~static_cast<uint32_t>(L.cand.pos[i]);
+  };
+  uint64_t edge = 0;
+  if (S.k < static_cast<uint32_t>(n))
+    edge = border_entry(L, V, n, bound, uint64_t(m_key) + 1, false, S.k, entry, units);
+  if (S.p < 1.0) {
+    if (whole < 0.0) {
+      double s = 0.0;
+      for (int i = tid; i < n; i += kRowThreads)
+        if (entry(i) >= edge) s += weight(L.cand.key[i]);
+      block_scan(s, L.wave_f64[2], whole);
+    }
+    const uint64_t target = max(static_cast<uint64_t>(ceil(S.p * whole * kUnit)), uint64_t(1));
+    edge = max(edge, border_entry(L, V, n, bound, uint64_t(m_key) + 1, true, target, entry, units));
+  }
+  // the draw: thread t holds candidates t * per .. in order of position
+  constexpr int kPerThread = kCandidates / kRowThreads;
+  const int per = (n + kRowThreads - 1) / kRowThreads;
+  double w[kPerThread], sum = 0.0, total;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = tid * per + j;
+    w[j] = 0.0;
+    if (j < per && i < n && entry(i) >= edge) {
+      w[j] = weight(L.cand.key[i]);
+      if (w[j] < S.q) w[j] = 0.0;
+    }
+    sum += w[j];
+  }
+  if (tid == 0) L.word[2] = 0xffffffffu, L.word[3] = 0;
+  __syncthreads();
+  double run = block_scan(sum, L.wave_f64[4], total);
   const double goal = S.u * total;
-  t = ties_before;
-  for (int i = c0; i < c1; ++i) {
-    const double w = kept(i, t);
-    acc += w;
-    if (w > 0.0) {
-      if (acc > goal) atomicMin(&L.word[2], static_cast<uint32_t>(i));
-      atomicMax(&L.word[3], static_cast<uint32_t>(i));
+  int hit = -1, last = -1;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    run += w[j];
+    if (w[j] > 0.0) {
+      if (hit < 0 && run > goal) hit = tid * per + j;
+      last = tid * per + j;
     }
   }
+  put_first(&L.word[2], hit >= 0, static_cast<uint32_t>(hit));
+  put_last(&L.word[3], last >= 0, static_cast<uint32_t>(last));
   __syncthreads();
   if (tid == 0) {
     const uint32_t i = L.word[2] != 0xffffffffu ? L.word[2] : L.word[3];
