@@ -656,6 +656,9 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
 }
 
 constexpr int kMaxGroups = 4096;
+constexpr int kDistanceBins = 1024;  // of bound_of_kth
+constexpr int kFineBits = kRowThreads == 512 ? 9 : 10;
+static_assert(1 << kFineBits == kRowThreads, "one of border_entry's bins per thread");
 constexpr int kMaxChunks = 64;
 
 struct PickLds {
@@ -672,7 +675,7 @@ struct PickLds {
     } half;  // the second half of the block's sums over the chunks
   };
   union {
-    uint32_t bins[kRowThreads];
+    uint32_t bins[kDistanceBins];
     uint32_t list[kCandidates];  // groups that reach the bound
     struct {  // finer histogram of the entries among which the border lies
       uint32_t count[kRowThreads];
@@ -696,20 +699,20 @@ struct PickLds {
 
 // Exclusive sum of v over the block in thread order; total gets the sum. One
 // barrier: `wave` must not have been in use since the last one. Every wave adds
-// up the 16 waves' sums in a row of its lanes.
+// up the waves' sums in a row of its lanes.
 template <class V>
 __device__ __forceinline__ V block_scan(V v, V* wave, V& total) {
-  static_assert(kRowWaves == 16, "one row of lanes");
+  static_assert(kRowWaves == 16 || kRowWaves == 8, "within a row of lanes");
   const V incl = wave_scan(v);
   const int lane = threadIdx.x & 63;
   if (lane == 63) wave[threadIdx.x >> 6] = incl;
   __syncthreads();
-  V w = wave[lane & 15];
+  V w = wave[lane & (kRowWaves - 1)];
   w += dpp<0x111>(w);
   w += dpp<0x112>(w);
   w += dpp<0x114>(w);
-  w += dpp<0x118>(w);
-  total = from_lane(w, 15);
+  if constexpr (kRowWaves == 16) w += dpp<0x118>(w);
+  total = from_lane(w, kRowWaves - 1);
   const int me = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const V base = me > 0 ? from_lane(w, me - 1) : V(0);
   return base + (incl - v);
@@ -893,18 +896,25 @@ __device__ __forceinline__ uint32_t distance_bin_end(uint32_t b) {
 // do. kMaskedKey + 1 where fewer than k groups hold an unmasked entry.
 __device__ __forceinline__ uint32_t bound_of_kth(PickLds& L, int groups, uint32_t m_key, uint32_t k) {
   const int tid = threadIdx.x;
-  L.bins[tid] = 0;
+  constexpr int kPer = kDistanceBins / kRowThreads;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) L.bins[tid + j * kRowThreads] = 0;
   if (tid == 0) L.word[0] = kMaskedKey + 1;
   __syncthreads();
   for (int g = tid; g < groups; g += kRowThreads)
     if (L.group_max[g] > kMaskedKey) atomicAdd(&L.bins[distance_bin(m_key - L.group_max[g])], 1u);
   __syncthreads();
-  const uint32_t mine = L.bins[tid];
-  uint32_t total;
-  const uint32_t before = block_scan(mine, L.wave_u32[1], total);
-  if (before < k && before + mine >= k) {
-    const uint32_t d = distance_bin_end(static_cast<uint32_t>(tid));
-    L.word[0] = max(kMaskedKey + 1, d < m_key ? m_key - d : 0u);
+  uint32_t mine[kPer], sum = 0, total;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) sum += mine[j] = L.bins[tid * kPer + j];
+  uint32_t before = block_scan(sum, L.wave_u32[1], total);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (before < k && before + mine[j] >= k) {
+      const uint32_t d = distance_bin_end(static_cast<uint32_t>(tid * kPer + j));
+      L.word[0] = max(kMaskedKey + 1, d < m_key ? m_key - d : 0u);
+    }
+    before += mine[j];
   }
   __syncthreads();
   return L.word[0];
@@ -1028,7 +1038,7 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
   if (tid < kScanBins) L.bin_scale[tid] = power(L, -tid);
   if (tid == 0) L.word[2] = 0xffffffffu;
   __syncthreads();
-  // the block's two halves take every second chunk
+  // the block's parts of kScanBins threads take turns at the chunks
   const int bin = tid % kScanBins;
   uint32_t count = 0;
   double mass = 0.0;
@@ -1055,10 +1065,12 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
       else rest += v * power(L, -(off[b] >= kScanBins ? off[b] + bin : bin + kScanBins));
     }
   }
-  if (tid >= kScanBins) L.half.count[bin] = count, L.half.mass[bin] = mass;
-  __syncthreads();
-  if (tid < kScanBins) count += L.half.count[bin], mass += L.half.mass[bin];
-  else count = 0, mass = 0.0;
+  if constexpr (kRowThreads > kScanBins) {
+    if (tid >= kScanBins) L.half.count[bin] = count, L.half.mass[bin] = mass;
+    __syncthreads();
+    if (tid < kScanBins) count += L.half.count[bin], mass += L.half.mass[bin];
+    else count = 0, mass = 0.0;
+  }
   const double scaled = tid < kScanBins ? mass * L.bin_scale[bin] : 0.0;
   double in_bins, rest_all;
   uint32_t counted;
@@ -1086,10 +1098,10 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
 // hi) amount to less than `target`: their number, or the units of their
 // weights. entry(i) = (key, ~position), 0 <= i < n, so that larger values come
 // first; at least one entry has a key in [lo, hi) and target > 0. The keys are
-// counted into 1024 bins, then those of the bin at which the target is reached
+// counted into a bin per thread, then those of the bin at which the target is reached
 // again, until that bin holds at most 64 entries, which one wave compares, or
-// entries of one key, of which the last one's position is looked for among
-// 1024 bins of positions. Returns the entry to every thread.
+// entries of one key, of which the last one's position is looked for among as
+// many bins of positions. Returns the entry to every thread.
 template <class Entry, class Units>
 __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint32_t lo, uint64_t hi, bool by_units,
                                                  uint64_t target, Entry entry, Units units) {
@@ -1099,7 +1111,7 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
   int count;
   for (;;) {
     const uint32_t span = static_cast<uint32_t>(hi - lo - 1);
-    const int shift = max(0, 22 - __clz(static_cast<int>(span | 1)));
+    const int shift = max(0, 32 - kFineBits - __clz(static_cast<int>(span | 1)));
     __syncthreads();
     L.fine.count[tid] = 0;
     L.fine.units[tid] = 0;
@@ -1177,14 +1189,14 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
       const uint64_t e = entry(i);
       const uint32_t pos = ~static_cast<uint32_t>(e);
       if (static_cast<uint32_t>(e >> 32) == lo && pos >> pos_shift == pos_bin) {
-        const uint32_t bit = pos & ((1u << pos_shift) - 1);  // below 256
+        const uint32_t bit = pos & ((1u << pos_shift) - 1);  // of at most 64 * 32
         atomicOr(&L.few[bit >> 5], 1u << (bit & 31));
       }
     }
     __syncthreads();
     if (tid == 0) {
       uint32_t nth = L.word[9], pos = pos_bin << pos_shift;
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 64; ++i) {
         uint32_t bits = L.few[i];
         const uint32_t c = static_cast<uint32_t>(__popc(bits));
         if (nth > c) {
