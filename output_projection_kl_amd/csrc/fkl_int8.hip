@@ -2,6 +2,7 @@
 // (fkl_quantize), and out = a_scale b_scale (A B^T) + bias over int8 operands
 // (fkl_project), A [M,K] and B [N,K] with k contiguous.
 #include <algorithm>
+#include <cstdlib>
 
 #include "fkl_decode.h"
 #include "fkl_device.h"
@@ -262,120 +263,275 @@ struct ProjectParams {
   DebugCheck dbg;  // debug build: span 0 = out, 1 = A, 2 = B, 3 = a_scale, 4 = b_scale, 5 = bias
 };
 
-__device__ __forceinline__ void store_as(const DebugCheck& d, float* p, float v) { dstore(d, 0, kDbgProjectOut, p, v); }
-__device__ __forceinline__ void store_as(const DebugCheck& d, __bf16* p, float v) {
-  dstore(d, 0, kDbgProjectOut, p, static_cast<__bf16>(v));
-}
-__device__ __forceinline__ void store_as(const DebugCheck& d, _Float16* p, float v) {
-  dstore(d, 0, kDbgProjectOut, p, static_cast<_Float16>(v));
+// One output element: the sum times a_scale (one rounding after the sum's
+// conversion), then one fused multiply-add, rounded to the output type.
+template <class T>
+__device__ __forceinline__ T scaled(int32_t sum, float sa, float sb, float bias) {
+  return static_cast<T>(fmaf(static_cast<float>(sum) * sa, sb, bias));
 }
 
-// Accumulators of one wave of a 256 x 256 int8 block tile: as MainAcc, in
-// 32-bit integers.
-using IntAcc = i32x4[8][2 * kNBW];
-
-// The bytes of a lane's 16-byte fragment (bytes 16 (lane >> 4) .. + 15 of the
-// last 64-byte stage) at and past `valid` cleared.
-__device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int valid, int lane) {
-  const int left = valid - 16 * (lane >> 4);
+// Bytes `valid` .. of a lane's 16 cleared.
+__device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int valid) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int n = left - 4 * j;
+    const int n = valid - 4 * j;
     v[j] &= n >= 4 ? -1 : n <= 0 ? 0 : (1 << (8 * n)) - 1;
   }
   return v;
 }
 
-// acc = A[m0 : m0 + 256] B[n0 : n0 + 256]^T: the ring of LDS stages and the
-// schedule of gemm_mainloop (fkl_device.h), each 64-byte stage row holding 64
-// int8 instead of 32 bf16, one v_mfma_i32_16x16x64_i8 step per stage. A and B
-// fragments use the same assignment of bytes to lanes, so any order of k
-// within a stage gives the same sum. In the last stage A's bytes at and past
-// K are cleared: what B holds there then does not matter.
-__device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int nk,
-                                              int last, IntAcc& acc, char* lds) {
-  using C = MainCfg;
-  constexpr int S = C::kStages;
-  constexpr int LA = C::kDmaA;
-  constexpr int LB = C::kDmaB;
-  constexpr int XA = 8;
-  constexpr int XB = 2 * kNBW;
+// ---- few rows -------------------------------------------------------------
+//
+// 16 MB rows of A against 16 columns of the output (rows of B) at a time, the
+// contraction split over the workgroup's 8 waves: wave w takes the F 64-byte
+// fragments from w F on of each span of 512 F bytes. B goes from memory
+// straight to the MFMA operands (lane l: row l & 15, 16 bytes at 16 (l >> 4)),
+// the next tile's while this one's are used; A's fragments stay in registers
+// where one span covers K. The waves' partial sums meet in LDS. HBM bound: B
+// is read once, at 8 F KiB per wave in flight.
+constexpr int kSkinnyWaves = 8;
+constexpr int kSkinnyThreads = 64 * kSkinnyWaves;
+
+template <class T, int MB, int F>
+__global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_project_skinny(ProjectParams P, int spans) {
+  __shared__ i32x4 part[2][kSkinnyWaves][MB][64];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int am = (wave / kWN) * 128;
-  const int bn = (wave % kWN) * 64;
-  const StageSrc<LA> sa = make_plain_src<kARows, LA>(A, m0, wave, lane);
-  const StageSrc<LB> sb = make_plain_src<C::kBExtent, LB>(B, n0, wave, lane);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MB);
+  const int8_t* const a = reinterpret_cast<const int8_t*>(P.A.base);
+  const int8_t* const b = reinterpret_cast<const int8_t*>(P.B.base);
+  const int64_t lda = P.A.ld * 2, ldb = P.B.ld * 2;
+  const int K16 = static_cast<int>(P.A.k_lim) * 2;
+  const int k_lane = wave * (F * 64) + (lane >> 4) * 16;
+
+  // A's bytes past K and rows past M are zero; what is read for B there then
+  // does not matter, and comes from inside B.
+  i32x4 fa[MB][F];
+  auto load_a = [&](int span) {
 #pragma unroll
-  for (int x = 0; x < XA; ++x)
+    for (int x = 0; x < MB; ++x) {
+      const int64_t m = m0 + x * 16 + (lane & 15);
 #pragma unroll
-    for (int y = 0; y < XB; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
-  block_barrier();
+      for (int f = 0; f < F; ++f) {
+        const int k = span * (kSkinnyWaves * F * 64) + k_lane + f * 64;
+        fa[x][f] = i32x4{0, 0, 0, 0};
+        if (m < P.M && k < P.K)
+          fa[x][f] = keep_bytes(dload(P.dbg, 1, kDbgProjectOperand, reinterpret_cast<const i32x4*>(a + m * lda + k)),
+                                P.K - k);
+      }
+    }
+  };
+  auto load_b = [&](int tile, int span, i32x4 (&fb)[F]) {
+    int64_t n = static_cast<int64_t>(tile) * 16 + (lane & 15);
+    n = n < P.N ? n : P.N - 1;
+    const int8_t* const row = b + n * ldb;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int k = span * (kSkinnyWaves * F * 64) + k_lane + f * 64;
+      fb[f] = dload(P.dbg, 2, kDbgProjectOperand, reinterpret_cast<const i32x4*>(row + (k < K16 ? k : 0)));
+    }
+  };
+  i32x4 acc[MB];
+  auto mma = [&](const i32x4 (&fb)[F]) {
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int x = 0; x < MB; ++x) acc[x] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[x][f], fb[f], acc[x], 0, 0, 0);
+  };
+  // The tile's sums: element e of 16 MB x 16 from the waves' accumulators
+  // (lane l of wave w: column l & 15, rows 4 (l >> 4) .. + 3 of each block).
+  auto finish = [&](int tile, int turn) {
+#pragma unroll
+    for (int x = 0; x < MB; ++x) part[turn][wave][x][lane] = acc[x];
+    __syncthreads();
+    constexpr int kElems = MB * 256;
+#pragma unroll
+    for (int e0 = 0; e0 < kElems; e0 += kSkinnyThreads) {
+      const int e = e0 + tid;
+      const int row = e >> 4, col = e & 15;
+      const int64_t m = m0 + row, n = static_cast<int64_t>(tile) * 16 + col;
+      if (e < kElems && m < P.M && n < P.N) {
+        const int l = ((row & 15) >> 2) * 16 + col;
+        int32_t sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSkinnyWaves; ++w) sum += reinterpret_cast<const int32_t*>(&part[turn][w][row >> 4][l])[row & 3];
+        const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m);
+        const float sb = dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n);
+        const float bias = P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n) : 0.0f;
+        dstore(P.dbg, 0, kDbgProjectOut, static_cast<T*>(P.out) + m * P.ldo + n, scaled<T>(sum, sa, sb, bias));
+      }
+    }
+  };
+
+  const int step = gridDim.x;
+  int turn = 0;  // the two halves of `part` take turns: one barrier per tile
+  if (spans == 1) {
+    load_a(0);
+    i32x4 fb[2][F];
+    int tile = blockIdx.x;
+    load_b(tile, 0, fb[0]);
+    while (true) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (tile + step < P.nblocks) load_b(tile + step, 0, fb[1 - h]);
+#pragma unroll
+        for (int x = 0; x < MB; ++x) acc[x] = i32x4{0, 0, 0, 0};
+        mma(fb[h]);
+        finish(tile, h);
+        tile += step;
+        if (tile >= P.nblocks) return;
+      }
+    }
+  }
+  for (int tile = blockIdx.x; tile < P.nblocks; tile += step, turn ^= 1) {
+#pragma unroll
+    for (int x = 0; x < MB; ++x) acc[x] = i32x4{0, 0, 0, 0};
+    for (int span = 0; span < spans; ++span) {
+      i32x4 fb[F];
+      load_b(tile, span, fb);
+      load_a(span);
+      mma(fb);
+    }
+    finish(tile, turn);
+  }
+}
+
+// ---- block tiles ----------------------------------------------------------
+//
+// TM x TN of the output on WM x WN waves, through a ring of LDS stages of 64
+// bytes of the contraction per row (64 int8, one v_mfma_i32_16x16x64_i8 step),
+// filled by direct global->LDS loads in the layout of plain operands
+// (fkl_device.h). A and B fragments use the same assignment of bytes to lanes,
+// so any order of k within a stage gives the same sum; in the last stage A's
+// bytes past K are cleared, and what B holds there does not matter.
+template <int TM_, int TN_, int WM_, int WN_>
+struct IntTile {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int XA = TM / WM / 16;  // 16-row fragments of a wave
+  static constexpr int XB = TN / WN / 16;
+  static constexpr int kStageA = TM * 64;
+  static constexpr int kStage = (TM + TN) * 64;
+  static constexpr int S = 4;
+  static constexpr int LA = TM / 16 / kWaves;  // 16-byte loads per lane per stage
+  static constexpr int LB = TN / 16 / kWaves;
+  static constexpr int kOutCols = TN < 128 ? TN : 128;  // columns staged at once by the epilogue
+  static constexpr int kOutLd = kOutCols + 4;
+  static constexpr int kLds = S * kStage > TM * kOutLd * 4 ? S * kStage : TM * kOutLd * 4;
+  static_assert(LA * 16 * kWaves == TM && LB * 16 * kWaves == TN, "whole loads");
+};
+
+// acc = A[m0 : m0 + TM] B[n0 : n0 + TN]^T. Two sets of fragments: while the
+// MFMAs of stage kt run, the fragments of stage kt + 1 are read, so the matrix
+// pipe and LDS work at once. Per stage: wait for stage kt + 1's loads and this
+// wave's fragment reads, one barrier (every wave has read stage kt), the
+// fragment reads of stage kt + 1, the loads of stage kt + S into stage kt's
+// place, the MFMAs. (LDS reads come before the loads: the compiler makes a
+// read that follows a global->LDS load wait for it.)
+template <class C>
+__device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int nk,
+                                              int last, i32x4 (&acc)[C::XA][C::XB], char* lds) {
+  constexpr int S = C::S;
+  constexpr int kDma = C::LA + C::LB;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int am = (wave / C::WN) * (C::XA * 16);
+  const int bn = (wave % C::WN) * (C::XB * 16);
+  const StageSrc<C::LA> sa = make_plain_src<C::TM, C::LA>(A, m0, wave, lane);
+  const StageSrc<C::LB> sb = make_plain_src<C::TN, C::LB>(B, n0, wave, lane);
+#pragma unroll
+  for (int x = 0; x < C::XA; ++x)
+#pragma unroll
+    for (int y = 0; y < C::XB; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
 #pragma unroll
   for (int p = 0; p < S; ++p) {
-    issue_stage<LA>(sa, p, p < nk, lds + p * C::kStageBytes, wave);
-    issue_stage<LB>(sb, p, p < nk, lds + p * C::kStageBytes + kAStageBytes, wave);
+    issue_stage<C::LA>(sa, p, p < nk, lds + p * C::kStage, wave);
+    issue_stage<C::LB>(sb, p, p < nk, lds + p * C::kStage + C::kStageA, wave);
   }
-  wait_vmcnt<(S - 1) * C::kDmaStage>();
-  block_barrier();
-  i32x4 a[XA], b[XB];
-  auto read = [&](const char* st) {
+  struct Set {
+    i32x4 a[C::XA], b[C::XB];
+  } f[2];
+  auto read = [&](Set& t, int kt) {
+    const char* st = lds + (kt % S) * C::kStage;
 #pragma unroll
-    for (int x = 0; x < XA; ++x) a[x] = __builtin_bit_cast(i32x4, frag_plain(st, am + x * 16, lane));
+    for (int x = 0; x < C::XA; ++x) t.a[x] = __builtin_bit_cast(i32x4, frag_plain(st, am + x * 16, lane));
 #pragma unroll
-    for (int y = 0; y < XB; ++y) b[y] = __builtin_bit_cast(i32x4, frag_plain(st + kAStageBytes, bn + y * 16, lane));
+    for (int y = 0; y < C::XB; ++y) t.b[y] = __builtin_bit_cast(i32x4, frag_plain(st + C::kStageA, bn + y * 16, lane));
   };
-  auto mma = [&] {
+  auto mma = [&](const Set& t) {
 #pragma unroll
-    for (int x = 0; x < XA; ++x)
+    for (int x = 0; x < C::XA; ++x)
 #pragma unroll
-      for (int y = 0; y < XB; ++y) acc[x][y] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[x], b[y], acc[x][y], 0, 0, 0);
+      for (int y = 0; y < C::XB; ++y)
+        acc[x][y] = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.a[x], t.b[y], acc[x][y], 0, 0, 0);
   };
-  read(lds);
-  for (int kt = 0; kt + 1 < nk; ++kt) {
-    char* cur = lds + (kt % S) * C::kStageBytes;
-    const char* nxt = lds + ((kt + 1) % S) * C::kStageBytes;
-    mma();
-    wait_vmcnt<(S - 2) * C::kDmaStage>();
+  auto step = [&](Set& cur, Set& next, int kt) {
+    wait_vmcnt<(S - 2) * kDma>();  // stage kt + 1 landed
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): stage kt's fragments are here
     block_barrier();
-    read(nxt);
+    read(next, kt + 1);
     const bool live = kt + S < nk;
-    issue_stage<LA>(sa, kt + S, live, cur, wave);
-    issue_stage<LB>(sb, kt + S, live, cur + kAStageBytes, wave);
-  }
+    char* place = lds + (kt % S) * C::kStage;
+    issue_stage<C::LA>(sa, kt + S, live, place, wave);
+    issue_stage<C::LB>(sb, kt + S, live, place + C::kStageA, wave);
+    mma(cur);
+  };
+  auto tail = [&](Set& t) {
 #pragma unroll
-  for (int x = 0; x < XA; ++x) a[x] = keep_bytes(a[x], last, lane);
-  mma();
+    for (int x = 0; x < C::XA; ++x) t.a[x] = keep_bytes(t.a[x], last - 16 * (lane >> 4));
+    mma(t);
+  };
+  wait_vmcnt<(S - 1) * kDma>();
+  block_barrier();
+  read(f[0], 0);
+  int kt = 0;
+  for (; kt + 2 < nk; kt += 2) {
+    step(f[0], f[1], kt);
+    step(f[1], f[0], kt + 1);
+  }
+  if (kt + 1 < nk) {
+    step(f[0], f[1], kt);
+    tail(f[1]);
+  } else {
+    tail(f[0]);
+  }
   wait_vmcnt<0>();
   block_barrier();
 }
 
-// One 256 x 256 output tile per workgroup. MFMA bound.
-template <class T>
-__global__ __launch_bounds__(kBlockThreads, 1) void k_project(ProjectParams P) {
-  __shared__ __align__(16) char lds[kKernelLdsBytes];
+// One output tile per workgroup. MFMA bound for the large tiles.
+template <class T, class C>
+__global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
+  __shared__ __align__(16) char lds[C::kLds];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
-  const int wm = wave / kWN;
-  const int wn = wave % kWN;
+  const int wm = wave / C::WN;
+  const int wn = wave % C::WN;
   int mbi, nbi;
   grouped_tile(xcd_contiguous(blockIdx.x, P.mblocks * P.nblocks), P.mblocks, P.nblocks, 8, mbi, nbi);
-  const int64_t m0 = static_cast<int64_t>(mbi) * kTile;
-  const int64_t n0 = static_cast<int64_t>(nbi) * kTile;
-  IntAcc acc;
-  dcheck_operand(P.dbg, 1, P.A, m0, kARows, false);
-  dcheck_operand(P.dbg, 2, P.B, n0, kTile, false);
-  int8_mainloop(P.A, P.B, m0, n0, P.nk, P.K - 64 * (P.nk - 1), acc, lds);
-  // Epilogue: each 256 x 128 half tile of sums staged in LDS, then scaled and
-  // stored with 32 lanes on 128 consecutive columns.
+  const int64_t m0 = static_cast<int64_t>(mbi) * C::TM;
+  const int64_t n0 = static_cast<int64_t>(nbi) * C::TN;
+  i32x4 acc[C::XA][C::XB];
+  dcheck_operand(P.dbg, 1, P.A, m0, C::TM, false);
+  dcheck_operand(P.dbg, 2, P.B, n0, C::TN, false);
+  int8_mainloop<C>(P.A, P.B, m0, n0, P.nk, P.K - 64 * (P.nk - 1), acc, lds);
+  // Epilogue: kOutCols columns of sums at a time staged in LDS, then scaled and
+  // stored with neighbouring lanes on neighbouring columns, 4 each.
   int32_t* stage = reinterpret_cast<int32_t*>(lds);
-  const int rmax = static_cast<int>(min<int64_t>(kTile, P.M - m0));
-  for (int half = 0; half < 2; ++half) {
-    const int64_t cbase = n0 + half * 128;
-    const int cmax = static_cast<int>(min<int64_t>(128, P.N - cbase));
-    const int c4 = (tid & 31) * 4;
+  const int rmax = static_cast<int>(min<int64_t>(C::TM, P.M - m0));
+  constexpr int kLanes = C::kOutCols / 4;  // lanes per row
+  constexpr int kWaveCols = C::XB * 16;
+  const int c4 = (tid % kLanes) * 4;
+  T* const out = static_cast<T*>(P.out);
+  const bool whole = P.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(P.out) % (4 * sizeof(T)) == 0;
+  for (int c0 = 0; c0 < C::TN; c0 += C::kOutCols) {
+    const int64_t cbase = n0 + c0;
+    const int cmax = static_cast<int>(min<int64_t>(C::kOutCols, P.N - cbase));
+    if (cmax <= 0) break;
     float sb[4], bias[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -383,27 +539,89 @@ __global__ __launch_bounds__(kBlockThreads, 1) void k_project(ProjectParams P) {
       sb[j] = in ? dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + cbase + c4 + j) : 0.0f;
       bias[j] = in && P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + cbase + c4 + j) : 0.0f;
     }
-    if ((wn >> 1) == half) {
-      const int cw = (wn & 1) * 64;
+    const int w0 = wn * kWaveCols - c0;  // this wave's first column among the staged ones
+    if (w0 >= 0 && w0 < C::kOutCols) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < C::XA; ++x)
 #pragma unroll
-        for (int y = 0; y < 2 * kNBW; ++y)
+        for (int y = 0; y < C::XB; ++y)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            stage[(wm * 128 + acc_row(x, i, lane)) * kStageLd + cw + acc_col(y, lane)] = acc[x][y][i];
+            stage[(wm * (C::XA * 16) + acc_row(x, i, lane)) * C::kOutLd + w0 + acc_col(y, lane)] = acc[x][y][i];
     }
     __syncthreads();
-    for (int r = tid >> 5; r < rmax; r += kBlockThreads / 32) {
+    for (int r = tid / kLanes; r < rmax; r += C::kThreads / kLanes) {
       const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m0 + r);
-      const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * kStageLd + c4);
-      T* o = static_cast<T*>(P.out) + (m0 + r) * P.ldo + cbase + c4;
+      const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * C::kOutLd + c4);
+      T* o = out + (m0 + r) * P.ldo + cbase + c4;
+      if (whole && c4 + 4 <= cmax) {
+        typedef T T4 __attribute__((ext_vector_type(4)));
+        dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<T4*>(o),
+               T4{scaled<T>(v[0], sa, sb[0], bias[0]), scaled<T>(v[1], sa, sb[1], bias[1]),
+                  scaled<T>(v[2], sa, sb[2], bias[2]), scaled<T>(v[3], sa, sb[3], bias[3])});
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c4 + j < cmax) store_as(P.dbg, o + j, fmaf(static_cast<float>(v[j]) * sa, sb[j], bias[j]));
+        for (int j = 0; j < 4; ++j)
+          if (c4 + j < cmax) dstore(P.dbg, 0, kDbgProjectOut, o + j, scaled<T>(v[j], sa, sb[j], bias[j]));
+      }
     }
     __syncthreads();
   }
+}
+
+using Tile256 = IntTile<256, 256, 2, 2>;
+using Tile256x128 = IntTile<256, 128, 2, 2>;
+using Tile256w8 = IntTile<256, 256, 2, 4>;
+using Tile256x128w8 = IntTile<256, 128, 4, 2>;
+using Tile128x256w8 = IntTile<128, 256, 2, 4>;
+using Tile128 = IntTile<128, 128, 2, 2>;
+using Tile64 = IntTile<64, 64, 2, 2>;
+
+template <class T, class C>
+static void launch_tiles(ProjectParams P, hipStream_t st) {
+  P.mblocks = static_cast<int32_t>(ceil_div(P.M, C::TM));
+  P.nblocks = static_cast<int32_t>(ceil_div(P.N, C::TN));
+  hipLaunchKernelGGL((k_project<T, C>), dim3(static_cast<unsigned>(P.mblocks) * P.nblocks), dim3(C::kThreads), 0, st,
+                     P);
+}
+
+template <class T, int MB>
+static void launch_skinny(ProjectParams P, hipStream_t st) {
+  P.nblocks = static_cast<int32_t>(ceil_div(P.N, 16));
+  P.mblocks = static_cast<int32_t>(ceil_div(P.M, 16 * MB));
+  const int per_wave = static_cast<int>(ceil_div(P.nk, kSkinnyWaves));
+  // as many workgroups as fit on the CUs at once, in all
+  const int resident = 2 * kTargetBlocks;
+  const dim3 grid(static_cast<unsigned>(std::min(P.nblocks, std::max(1, resident / P.mblocks))),
+                  static_cast<unsigned>(P.mblocks));
+  const dim3 block(kSkinnyThreads);
+  if (per_wave <= 2) hipLaunchKernelGGL((k_project_skinny<T, MB, 2>), grid, block, 0, st, P, 1);
+  else if (per_wave <= 4) hipLaunchKernelGGL((k_project_skinny<T, MB, 4>), grid, block, 0, st, P, 1);
+  else
+    hipLaunchKernelGGL((k_project_skinny<T, MB, 8>), grid, block, 0, st, P,
+                       static_cast<int>(ceil_div(P.nk, 8 * kSkinnyWaves)));
+}
+
+static int forced_variant() {
+  const char* v = std::getenv("FKL_VARIANT");
+  return v ? std::atoi(v) : 0;
+}
+
+template <class T>
+static void launch_product(const ProjectParams& P, hipStream_t st) {
+  const int v = forced_variant();
+  if (v ? v == 1 : P.M <= 16) return launch_skinny<T, 1>(P, st);
+  if (v ? v == 2 : P.M <= 32) return launch_skinny<T, 2>(P, st);
+  if (v ? v == 3 : P.M <= 64) return launch_skinny<T, 4>(P, st);
+  if (v == 8) return launch_tiles<T, Tile256w8>(P, st);
+  if (v == 9) return launch_tiles<T, Tile256x128w8>(P, st);
+  if (v == 10) return launch_tiles<T, Tile128x256w8>(P, st);
+  if (v == 7) return launch_tiles<T, Tile64>(P, st);
+  auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(P.M, tm) * ceil_div(P.N, tn); };
+  if (v ? v == 4 : tiles(256, 256) >= kTargetBlocks) return launch_tiles<T, Tile256>(P, st);
+  if (v ? v == 5 : tiles(256, 128) >= kTargetBlocks) return launch_tiles<T, Tile256x128>(P, st);
+  if (v ? v == 6 : tiles(128, 128) >= kTargetBlocks) return launch_tiles<T, Tile128>(P, st);
+  launch_tiles<T, Tile64>(P, st);
 }
 
 hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_t st) {
@@ -444,8 +662,7 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   P.a_scale = a_scale, P.b_scale = g.b_scale, P.bias = g.bias;
   P.out = g.out;
   P.ldo = p.ldo, P.M = p.M, P.N = p.N;
-  P.mblocks = static_cast<int32_t>(ceil_div(p.M, kTile));
-  P.nblocks = static_cast<int32_t>(ceil_div(p.N, kTile));
+  P.mblocks = P.nblocks = 0;  // by the variant
   const uint64_t out_bytes = static_cast<uint64_t>((p.M - 1) * p.ldo + p.N) * type_bytes(p.out_type);
   P.dbg = make_debug_check(word, {{g.out, out_bytes},
                                   {a, static_cast<uint64_t>((p.M - 1) * lda + row16)},
@@ -457,8 +674,9 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   const double bytes = static_cast<double>(p.M) * p.K + static_cast<double>(p.N) * p.K +
                        static_cast<double>(p.M) * p.N * type_bytes(p.out_type);
   TraceScope ts(st, "project", flops, bytes);
-  auto* k = p.out_type == FKL_F32 ? k_project<float> : p.out_type == FKL_BF16 ? k_project<__bf16> : k_project<_Float16>;
-  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(P.mblocks) * P.nblocks), dim3(kBlockThreads), 0, st, P);
+  if (p.out_type == FKL_F32) launch_product<float>(P, st);
+  else if (p.out_type == FKL_BF16) launch_product<__bf16>(P, st);
+  else launch_product<_Float16>(P, st);
   return hipGetLastError();
 }
 
