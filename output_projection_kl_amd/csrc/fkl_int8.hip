@@ -399,118 +399,206 @@ __global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_projec
 
 // ---- block tiles ----------------------------------------------------------
 //
-// TM x TN of the output on WM x WN waves, through a ring of LDS stages of 64
-// bytes of the contraction per row (64 int8, one v_mfma_i32_16x16x64_i8 step),
-// filled by direct global->LDS loads in the layout of plain operands
-// (fkl_device.h). A and B fragments use the same assignment of bytes to lanes,
-// so any order of k within a stage gives the same sum; in the last stage A's
-// bytes past K are cleared, and what B holds there does not matter.
-template <int TM_, int TN_, int WM_, int WN_>
+// TM x TN of the output on WM x WN waves, through a ring of S LDS stages of
+// 128 bytes of the contraction per row: two v_mfma_i32_16x16x64_i8 steps. The
+// stages are filled by direct global->LDS loads of 16 bytes per lane, eight
+// lanes on one row's 128 bytes: whole cache lines. (With 64-byte stage rows,
+// as the bf16 tiles have them, each line is asked for twice, and the loads
+// alone took 210 of the 287 us of a 8192 x 8192 x 4096 product.)
+//
+// LDS: row r of a stage at 128 r, its 16-byte chunk c at physical chunk c ^
+// ((r >> 1) & 7): a fragment's 16 rows then lie on 16 distinct 16-byte groups
+// of the 256 bytes that the banks span. Fragments of A and B use the same
+// assignment of bytes to lanes, so any order of k within a step gives the same
+// sum; in the last stage A's bytes past K are cleared, and what B holds there
+// does not matter.
+constexpr int kIntStageK = 128;
+
+template <int TM_, int TN_, int WM_, int WN_, int S_>
 struct IntTile {
-  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int XA = TM / WM / 16;  // 16-row fragments of a wave
   static constexpr int XB = TN / WN / 16;
-  static constexpr int kStageA = TM * 64;
-  static constexpr int kStage = (TM + TN) * 64;
-  static constexpr int S = 4;
-  static constexpr int LA = TM / 16 / kWaves;  // 16-byte loads per lane per stage
-  static constexpr int LB = TN / 16 / kWaves;
-  static constexpr int kOutCols = TN < 128 ? TN : 128;  // columns staged at once by the epilogue
-  static constexpr int kOutLd = kOutCols + 4;
-  static constexpr int kLds = S * kStage > TM * kOutLd * 4 ? S * kStage : TM * kOutLd * 4;
-  static_assert(LA * 16 * kWaves == TM && LB * 16 * kWaves == TN, "whole loads");
+  static constexpr int kStageA = TM * kIntStageK;
+  static constexpr int kStage = (TM + TN) * kIntStageK;
+  static constexpr int LA = (TM / 8 + kWaves - 1) / kWaves;  // loads per lane per stage, 8 rows a wave each
+  static constexpr int LB = (TN / 8 + kWaves - 1) / kWaves;
+  static constexpr int kDma = LA + LB;
+  // where waves that have no rows left load to, so that every wave's count of loads is the same
+  static constexpr bool kSpare = LA * kWaves * 8 != TM || LB * kWaves * 8 != TN;
+  static constexpr int kRing = S * kStage + (kSpare ? 1024 * kWaves : 0);
+  static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0, "whole fragments");
+  // the epilogue's staging: rows of out_cols columns of the output type, 16 bytes apart from each other
+  static constexpr int out_cols(int size) { return TN * size < 512 ? TN : 512 / size; }
+  static constexpr int out_pitch(int size) { return out_cols(size) * size + 16; }
+  static constexpr int lds(int size) {
+    return kRing > TM * out_pitch(size) ? kRing : TM * out_pitch(size);
+  }
 };
 
-// acc = A[m0 : m0 + TM] B[n0 : n0 + TN]^T. Two sets of fragments: while the
-// MFMAs of stage kt run, the fragments of stage kt + 1 are read, so the matrix
-// pipe and LDS work at once. Per stage: wait for stage kt + 1's loads and this
-// wave's fragment reads, one barrier (every wave has read stage kt), the
-// fragment reads of stage kt + 1, the loads of stage kt + S into stage kt's
-// place, the MFMAs. (LDS reads come before the loads: the compiler makes a
-// read that follows a global->LDS load wait for it.)
+// One operand's stage loads of a wave: load j covers rows 8 (wave L + j) .. + 7
+// of the tile's R rows.
+template <int L>
+struct IntSrc {
+  const int8_t* base;
+  int32_t bytes;  // of the rows inside the operand; what lies past them reads as zero
+  uint32_t off[L];
+  int32_t chunk;  // first byte of the lane's chunk within the stage
+  int32_t k_lim;
+};
+
+template <int R, int L>
+__device__ __forceinline__ IntSrc<L> int_src(const Operand& op, int64_t row0, int wave, int lane) {
+  IntSrc<L> s;
+  const OperandView v = plain_view(op, row0, R);
+  s.base = reinterpret_cast<const int8_t*>(v.base);
+  s.bytes = static_cast<int32_t>(v.bytes);
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    const int r = (wave * L + j) * 8 + (lane >> 3);
+    s.off[j] = r < R ? static_cast<uint32_t>(r * op.ld * 2) : kOob;
+  }
+  s.chunk = (lane & 7) << 4;
+  s.k_lim = static_cast<int32_t>(op.k_lim) * 2;
+  return s;
+}
+
+// Issues stage kt of one operand into its LDS region; every lane reads out of
+// range (zeros, no memory access) where live is false.
+template <int R, int L>
+__device__ __forceinline__ void issue_int(const IntSrc<L>& s, int kt, bool live, char* region, char* spare, int wave,
+                                          int lane) {
+  const __amdgpu_buffer_rsrc_t rsrc =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(s.base), 0, s.bytes, 0x00020000);
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    const int block = wave * L + j;
+    const int r = block * 8 + (lane >> 3);
+    const int k = kt * kIntStageK + (s.chunk ^ (((r >> 1) & 7) << 4));
+    uint32_t off = s.off[j] + static_cast<uint32_t>(k);
+    if (!live || k >= s.k_lim || s.off[j] == kOob) off = kOob;
+    char* dst = block * 8 < R ? region + block * 1024 : spare + wave * 1024;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (FKL_LDS void*)dst, 16, static_cast<int>(off), 0, 0, 0);
+  }
+}
+
+// Fragment of 16 rows x 64 bytes, step kk of a stage: lane l receives row l &
+// 15, bytes 16 (l >> 4) .. + 15.
+__device__ __forceinline__ i32x4 int_frag(const char* region, int row0, int kk, int lane) {
+  const int r = row0 + (lane & 15);
+  const int c = kk * 4 + (lane >> 4);
+  return *reinterpret_cast<const i32x4*>(region + r * kIntStageK + ((c ^ ((r >> 1) & 7)) << 4));
+}
+
+// acc = A[m0 : m0 + TM] B[n0 : n0 + TN]^T, with B as the MFMA's first operand:
+// lane l then holds four consecutive columns 4 (l >> 4) .. + 3 of row l & 15 of
+// each 16 x 16 block. Two sets of fragments: while the
+// MFMAs of one step run, the fragments of the next are read, so that the
+// matrix pipe and LDS work at once; the order of issue is fixed by hand (left
+// alone, the compiler gathers the reads at the end). Per stage one barrier, at
+// its second step: every wave holds all of its fragments of the stage, whose
+// place then takes the loads of stage kt + S, and has waited for its own loads
+// of stage kt + 1. (LDS reads come before the loads: the compiler makes a read
+// that follows a global->LDS load wait for it.)
 template <class C>
-__device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int nk,
-                                              int last, i32x4 (&acc)[C::XA][C::XB], char* lds) {
+__device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int K,
+                                              i32x4 (&acc)[C::XA][C::XB], char* lds) {
   constexpr int S = C::S;
-  constexpr int kDma = C::LA + C::LB;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int am = (wave / C::WN) * (C::XA * 16);
   const int bn = (wave % C::WN) * (C::XB * 16);
-  const StageSrc<C::LA> sa = make_plain_src<C::TM, C::LA>(A, m0, wave, lane);
-  const StageSrc<C::LB> sb = make_plain_src<C::TN, C::LB>(B, n0, wave, lane);
-#pragma unroll
-  for (int x = 0; x < C::XA; ++x)
-#pragma unroll
-    for (int y = 0; y < C::XB; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
-#pragma unroll
-  for (int p = 0; p < S; ++p) {
-    issue_stage<C::LA>(sa, p, p < nk, lds + p * C::kStage, wave);
-    issue_stage<C::LB>(sb, p, p < nk, lds + p * C::kStage + C::kStageA, wave);
-  }
+  const int n_stages = (K + kIntStageK - 1) / kIntStageK;
+  const IntSrc<C::LA> sa = int_src<C::TM, C::LA>(A, m0, wave, lane);
+  const IntSrc<C::LB> sb = int_src<C::TN, C::LB>(B, n0, wave, lane);
+  char* const spare = lds + S * C::kStage;
+  auto issue = [&](int kt) {
+    char* place = lds + (kt % S) * C::kStage;
+    issue_int<C::TM, C::LA>(sa, kt, kt < n_stages, place, spare, wave, lane);
+    issue_int<C::TN, C::LB>(sb, kt, kt < n_stages, place + C::kStageA, spare, wave, lane);
+  };
   struct Set {
     i32x4 a[C::XA], b[C::XB];
   } f[2];
-  auto read = [&](Set& t, int kt) {
+  auto read = [&](Set& t, int kt, int kk) {
     const char* st = lds + (kt % S) * C::kStage;
 #pragma unroll
-    for (int x = 0; x < C::XA; ++x) t.a[x] = __builtin_bit_cast(i32x4, frag_plain(st, am + x * 16, lane));
+    for (int x = 0; x < C::XA; ++x) t.a[x] = int_frag(st, am + x * 16, kk, lane);
 #pragma unroll
-    for (int y = 0; y < C::XB; ++y) t.b[y] = __builtin_bit_cast(i32x4, frag_plain(st + C::kStageA, bn + y * 16, lane));
+    for (int y = 0; y < C::XB; ++y) t.b[y] = int_frag(st + C::kStageA, bn + y * 16, kk, lane);
   };
   auto mma = [&](const Set& t) {
 #pragma unroll
     for (int x = 0; x < C::XA; ++x)
 #pragma unroll
       for (int y = 0; y < C::XB; ++y)
-        acc[x][y] = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.a[x], t.b[y], acc[x][y], 0, 0, 0);
+        acc[x][y] = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.b[y], t.a[x], acc[x][y], 0, 0, 0);
   };
-  auto step = [&](Set& cur, Set& next, int kt) {
-    wait_vmcnt<(S - 2) * kDma>();  // stage kt + 1 landed
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): stage kt's fragments are here
-    block_barrier();
-    read(next, kt + 1);
-    const bool live = kt + S < nk;
-    char* place = lds + (kt % S) * C::kStage;
-    issue_stage<C::LA>(sa, kt + S, live, place, wave);
-    issue_stage<C::LB>(sb, kt + S, live, place + C::kStageA, wave);
-    mma(cur);
-  };
-  auto tail = [&](Set& t) {
 #pragma unroll
-    for (int x = 0; x < C::XA; ++x) t.a[x] = keep_bytes(t.a[x], last - 16 * (lane >> 4));
-    mma(t);
-  };
-  wait_vmcnt<(S - 1) * kDma>();
+  for (int x = 0; x < C::XA; ++x)
+#pragma unroll
+    for (int y = 0; y < C::XB; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int p = 0; p < S; ++p) issue(p);
+  wait_vmcnt<(S - 1) * C::kDma>();
   block_barrier();
-  read(f[0], 0);
-  int kt = 0;
-  for (; kt + 2 < nk; kt += 2) {
-    step(f[0], f[1], kt);
-    step(f[1], f[0], kt + 1);
+  read(f[0], 0, 0);
+  constexpr int kMfma = C::XA * C::XB;
+  constexpr int kReads = C::XA + C::XB;
+  constexpr int kFirst = kMfma >= kReads ? kMfma / kReads : 1;  // MFMAs per fragment read
+  constexpr int kSecond = kMfma >= kReads + C::kDma ? kMfma / (kReads + C::kDma) : 1;  // and with the loads
+  for (int kt = 0; kt + 1 < n_stages; ++kt) {
+    __builtin_amdgcn_sched_barrier(0);
+    read(f[1], kt, 1);
+    mma(f[0]);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kFirst, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<(S - 2) * C::kDma>();
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    block_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(f[0], kt + 1, 0);
+    issue(kt + S);
+    mma(f[1]);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kSecond, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < C::kDma; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kSecond, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
-  if (kt + 1 < nk) {
-    step(f[0], f[1], kt);
-    tail(f[1]);
-  } else {
-    tail(f[0]);
-  }
+  const int last = K - (n_stages - 1) * kIntStageK - 16 * (lane >> 4);  // bytes from the lane's chunk on
+  read(f[1], n_stages - 1, 1);
+#pragma unroll
+  for (int x = 0; x < C::XA; ++x) f[0].a[x] = keep_bytes(f[0].a[x], last), f[1].a[x] = keep_bytes(f[1].a[x], last - 64);
+  mma(f[0]);
+  mma(f[1]);
   wait_vmcnt<0>();
   block_barrier();
 }
 
-// One output tile per workgroup. MFMA bound for the large tiles.
+// One output tile per workgroup. MFMA bound for the large tiles. The results
+// are staged in LDS in the output's type and stored as whole lines: stored
+// from the registers (32 bytes of a row at a time) they took a 8192 x 128256 x
+// 4096 product from 4.09 to 4.58 ms.
 template <class T, class C>
 __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
-  __shared__ __align__(16) char lds[C::kLds];
+  __shared__ __align__(16) char lds[C::lds(sizeof(T))];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
-  const int wm = wave / C::WN;
-  const int wn = wave % C::WN;
   int mbi, nbi;
   grouped_tile(xcd_contiguous(blockIdx.x, P.mblocks * P.nblocks), P.mblocks, P.nblocks, 8, mbi, nbi);
   const int64_t m0 = static_cast<int64_t>(mbi) * C::TM;
@@ -518,64 +606,78 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
   i32x4 acc[C::XA][C::XB];
   dcheck_operand(P.dbg, 1, P.A, m0, C::TM, false);
   dcheck_operand(P.dbg, 2, P.B, n0, C::TN, false);
-  int8_mainloop<C>(P.A, P.B, m0, n0, P.nk, P.K - 64 * (P.nk - 1), acc, lds);
-  // Epilogue: kOutCols columns of sums at a time staged in LDS, then scaled and
-  // stored with neighbouring lanes on neighbouring columns, 4 each.
-  int32_t* stage = reinterpret_cast<int32_t*>(lds);
-  const int rmax = static_cast<int>(min<int64_t>(C::TM, P.M - m0));
-  constexpr int kLanes = C::kOutCols / 4;  // lanes per row
-  constexpr int kWaveCols = C::XB * 16;
-  const int c4 = (tid % kLanes) * 4;
-  T* const out = static_cast<T*>(P.out);
-  const bool whole = P.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(P.out) % (4 * sizeof(T)) == 0;
-  for (int c0 = 0; c0 < C::TN; c0 += C::kOutCols) {
-    const int64_t cbase = n0 + c0;
-    const int cmax = static_cast<int>(min<int64_t>(C::kOutCols, P.N - cbase));
-    if (cmax <= 0) break;
-    float sb[4], bias[4];
+  int8_mainloop<C>(P.A, P.B, m0, n0, P.K, acc, lds);
+  constexpr int kCols = C::out_cols(sizeof(T));
+  constexpr int kPitch = C::out_pitch(sizeof(T));
+  constexpr int kPer = 16 / sizeof(T);     // elements of a 16-byte piece
+  constexpr int kLanes = kCols / kPer;     // pieces of a staged row
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  const int m_wave = (wave / C::WN) * (C::XA * 16) + (lane & 15);  // of this lane's rows within the tile
+  const int n_wave = (wave % C::WN) * (C::XB * 16) + 4 * (lane >> 4);
+  float sa[C::XA];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = c4 + j < cmax;
-      sb[j] = in ? dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + cbase + c4 + j) : 0.0f;
-      bias[j] = in && P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + cbase + c4 + j) : 0.0f;
-    }
-    const int w0 = wn * kWaveCols - c0;  // this wave's first column among the staged ones
-    if (w0 >= 0 && w0 < C::kOutCols) {
+  for (int x = 0; x < C::XA; ++x) {
+    const int64_t m = m0 + m_wave + x * 16;
+    sa[x] = m < P.M ? dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m) : 0.0f;
+  }
+  T* const out = static_cast<T*>(P.out) + m0 * P.ldo + n0;
+  const bool whole = P.ldo % kPer == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0;
+  const int rmax = static_cast<int>(min<int64_t>(C::TM, P.M - m0));
+#pragma unroll
+  for (int c0 = 0; c0 < C::TN; c0 += kCols) {
+    const int cmax = static_cast<int>(min<int64_t>(kCols, P.N - n0 - c0));
+    if (cmax <= 0) break;
+#pragma unroll
+    for (int y = 0; y < C::XB; ++y) {
+      const int col = n_wave + y * 16 - c0;
+      if (col < 0 || col >= kCols) continue;  // the same for the whole wave
+      float sb[4], bias[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = col + j < cmax;
+        sb[j] = in ? dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n0 + c0 + col + j) : 0.0f;
+        bias[j] = in && P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n0 + c0 + col + j) : 0.0f;
+      }
 #pragma unroll
       for (int x = 0; x < C::XA; ++x)
-#pragma unroll
-        for (int y = 0; y < C::XB; ++y)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            stage[(wm * (C::XA * 16) + acc_row(x, i, lane)) * C::kOutLd + w0 + acc_col(y, lane)] = acc[x][y][i];
+        *reinterpret_cast<T4*>(lds + (m_wave + x * 16) * kPitch + col * static_cast<int>(sizeof(T))) =
+            T4{scaled<T>(acc[x][y][0], sa[x], sb[0], bias[0]), scaled<T>(acc[x][y][1], sa[x], sb[1], bias[1]),
+               scaled<T>(acc[x][y][2], sa[x], sb[2], bias[2]), scaled<T>(acc[x][y][3], sa[x], sb[3], bias[3])};
     }
     __syncthreads();
-    for (int r = tid / kLanes; r < rmax; r += C::kThreads / kLanes) {
-      const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m0 + r);
-      const i32x4 v = *reinterpret_cast<const i32x4*>(stage + r * C::kOutLd + c4);
-      T* o = out + (m0 + r) * P.ldo + cbase + c4;
-      if (whole && c4 + 4 <= cmax) {
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<T4*>(o),
-               T4{scaled<T>(v[0], sa, sb[0], bias[0]), scaled<T>(v[1], sa, sb[1], bias[1]),
-                  scaled<T>(v[2], sa, sb[2], bias[2]), scaled<T>(v[3], sa, sb[3], bias[3])});
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c4 + j < cmax) dstore(P.dbg, 0, kDbgProjectOut, o + j, scaled<T>(v[j], sa, sb[j], bias[j]));
+    if (whole) {
+      const int c = (tid % kLanes) * kPer;
+      for (int r = tid / kLanes; r < rmax; r += C::kThreads / kLanes) {
+        const char* const from = lds + r * kPitch + c * static_cast<int>(sizeof(T));
+        T* const to = out + r * P.ldo + c0 + c;
+        if (c + kPer <= cmax) {
+          dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<u32x4*>(to), *reinterpret_cast<const u32x4*>(from));
+        } else {
+          for (int j = 0; c + j < cmax; ++j)
+            dstore(P.dbg, 0, kDbgProjectOut, to + j, reinterpret_cast<const T*>(from)[j]);
+        }
       }
+    } else {  // rows that do not start at 16 bytes: neighbouring lanes on neighbouring elements
+      constexpr int kAcross = kCols < C::kThreads ? kCols : C::kThreads;
+      for (int r = tid / kAcross; r < rmax; r += C::kThreads / kAcross)
+        for (int c = tid % kAcross; c < cmax; c += kAcross)
+          dstore(P.dbg, 0, kDbgProjectOut, out + r * P.ldo + c0 + c,
+                 reinterpret_cast<const T*>(lds + r * kPitch)[c]);
     }
-    __syncthreads();
+    if (c0 + kCols < C::TN) __syncthreads();
   }
 }
 
-using Tile256 = IntTile<256, 256, 2, 2>;
-using Tile256x128 = IntTile<256, 128, 2, 2>;
-using Tile256w8 = IntTile<256, 256, 2, 4>;
-using Tile256x128w8 = IntTile<256, 128, 4, 2>;
-using Tile128x256w8 = IntTile<128, 256, 2, 4>;
-using Tile128 = IntTile<128, 128, 2, 2>;
-using Tile64 = IntTile<64, 64, 2, 2>;
+using Tile256 = IntTile<256, 256, 2, 4, 2>;
+using Tile256x128 = IntTile<256, 128, 4, 2, 3>;
+using Tile128x256 = IntTile<128, 256, 2, 4, 3>;
+using Tile128 = IntTile<128, 128, 2, 2, 2>;
+using Tile128s4 = IntTile<128, 128, 2, 2, 4>;
+using Tile64 = IntTile<64, 64, 2, 2, 3>;
+using Tile64x128 = IntTile<64, 128, 2, 2, 3>;
+using Tile32x128 = IntTile<32, 128, 1, 4, 3>;
+using Tile16x128 = IntTile<16, 128, 1, 4, 4>;
+using Tile16x64 = IntTile<16, 64, 1, 4, 4>;
 
 template <class T, class C>
 static void launch_tiles(ProjectParams P, hipStream_t st) {
@@ -613,10 +715,13 @@ static void launch_product(const ProjectParams& P, hipStream_t st) {
   if (v ? v == 1 : P.M <= 16) return launch_skinny<T, 1>(P, st);
   if (v ? v == 2 : P.M <= 32) return launch_skinny<T, 2>(P, st);
   if (v ? v == 3 : P.M <= 64) return launch_skinny<T, 4>(P, st);
-  if (v == 8) return launch_tiles<T, Tile256w8>(P, st);
-  if (v == 9) return launch_tiles<T, Tile256x128w8>(P, st);
-  if (v == 10) return launch_tiles<T, Tile128x256w8>(P, st);
   if (v == 7) return launch_tiles<T, Tile64>(P, st);
+  if (v == 8) return launch_tiles<T, Tile128s4>(P, st);
+  if (v == 10) return launch_tiles<T, Tile128x256>(P, st);
+  if (v == 11) return launch_tiles<T, Tile64x128>(P, st);
+  if (v == 12) return launch_tiles<T, Tile32x128>(P, st);
+  if (v == 13) return launch_tiles<T, Tile16x128>(P, st);
+  if (v == 14) return launch_tiles<T, Tile16x64>(P, st);
   auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(P.M, tm) * ceil_div(P.N, tn); };
   if (v ? v == 4 : tiles(256, 256) >= kTargetBlocks) return launch_tiles<T, Tile256>(P, st);
   if (v ? v == 5 : tiles(256, 128) >= kTargetBlocks) return launch_tiles<T, Tile256x128>(P, st);
