@@ -28,12 +28,28 @@ enum DecodeDebugBit : uint32_t {
 };
 constexpr int kDecodeDebugBits = 6;
 
+// How the product is laid out on the GPU: the split-contraction kernel for few
+// output elements, or block tiles.
+enum ProjectShapeId {
+  kProjectSkinny,
+  kProject16x64,
+  kProject64,
+  kProject64x128,
+  kProject128,
+  kProject128x256,
+  kProject256x128,
+  kProject256
+};
+
 struct ProjectPlan {
   int64_t M, N, K, lda, ldb, ldo;
   int a_type, out_type;
   bool a_copied, b_copied;  // the 8-bit operand is copied to rows of round_up(K, 16) bytes
-  // workspace offsets (bytes): the quantised or copied a, its scales, the copied b
-  size_t off_a, off_a_scale, off_b, bytes;
+  ProjectShapeId shape;
+  int splits;       // of the contraction, each of k_split bytes (1: none)
+  int64_t k_split;
+  // workspace offsets (bytes): the quantised or copied a, its scales, the copied b, the splits' sums
+  size_t off_a, off_a_scale, off_b, off_sums, bytes;
 };
 
 struct ProjectArgs {

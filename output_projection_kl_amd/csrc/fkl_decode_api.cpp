@@ -1,6 +1,7 @@
 // C ABI of the 8-bit head and of sampling: argument checks (pure host code,
 // no HIP call before they pass), workspace plans, dispatch to the launchers in
 // fkl_int8.hip and fkl_sample.hip.
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -70,6 +71,68 @@ fkl_status debug_end(char* ws, hipStream_t stream) {
 
 namespace fkl {
 
+// The layout with the least estimated time, us. A block tile's stage (128
+// bytes of the contraction) takes `filled` of a CU that as many workgroups
+// share as fit, and `alone` for a workgroup with a CU to itself, whichever is
+// longer over the rounds that the tiles take; then the tile is stored. The
+// constants are fitted to the times of every layout at 157 sizes (M 1 to 8192,
+// N 64 to 201088, K 64 to 8192): the layout that they pick took 1.5% longer
+// than the fastest one in the mean. Both sides at some of them: 8192 x 8192 x
+// 4096 (M, N, K): 232 us as 256 x 256, 292 as 128 x 256, 328 as 128 x 128; 2048
+// x 4096 x 4096: 51, 39 and 44; 201 x 32003 x 2887: 50, 36 and 41; 48 x 128256 x
+// 4096: 121 as 64 x 128, 118 as 64 x 64, 153 as 16 x 64; 1 x 201088 x 2880: 110,
+// 106 and 100; 5 x 1024 x 1024: 6.1 as 16 x 16, 7.3 as 16 x 64; 1 x 128 x 5120:
+// 8.7 as 16 x 16, 19.7 as 64 x 64, 10.8 of those with the contraction split.
+static void choose_project_shape(ProjectPlan* p) {
+  struct Tile {
+    ProjectShapeId id;
+    int tm, tn, per_cu;
+    double alone, filled;
+  };
+  static const Tile kTiles[] = {
+      {kProject16x64, 16, 64, 3, 0.21, 0.16},   {kProject64, 64, 64, 3, 0.28, 0.26},
+      {kProject64x128, 64, 128, 2, 0.80, 0.50}, {kProject128, 128, 128, 2, 0.85, 0.68},
+      {kProject128x256, 128, 256, 1, 0.75, 1.20}, {kProject256x128, 256, 128, 1, 0.76, 1.10},
+      {kProject256, 256, 256, 1, 1.07, 1.80},
+  };
+  const double kLaunch = 2.4;  // a launch's own time
+  const double kJoin = 4.2;    // the second launch of a split contraction
+  const double m = static_cast<double>(p->M), n = static_cast<double>(p->N), k = static_cast<double>(p->K);
+  const double memory = (n * k + m * k + m * n * type_bytes(p->out_type)) / 6.5e6;
+  const int64_t stages = ceil_div(p->K, 128);
+  p->splits = 1;
+  p->k_split = p->K;
+  // 16 x 16 tiles, two workgroups a CU: one tile's latency, then less for each
+  // further one; B is read again for every 16 rows
+  const int64_t small = ceil_div(p->M, 16) * ceil_div(p->N, 16);
+  p->shape = kProjectSkinny;
+  double best = kLaunch + 0.95 * k / 1024 + static_cast<double>(ceil_div(small, 512) - 1) * (0.29 * k / 1024 + 0.3);
+  best = std::max(best, static_cast<double>(ceil_div(p->M, 16)) * n * k / 3.6e6);
+  for (const Tile& t : kTiles) {
+    const int64_t tiles = ceil_div(p->M, t.tm) * ceil_div(p->N, t.tn);
+    const double rounds = static_cast<double>(ceil_div(tiles, int64_t(kTargetBlocks) * t.per_cu));
+    const double per_cu = static_cast<double>(tiles) / kTargetBlocks;
+    const double sums = static_cast<double>(stages) * std::max(t.alone * rounds, t.filled * per_cu);
+    const double store = 4.0 * t.tm * t.tn / 65536 * std::max(rounds, per_cu) * type_bytes(p->out_type) / 2;
+    // rows past M are computed in vain: a little even where memory decides
+    const double est = std::max(kLaunch + sums + store, memory) + 0.02 * sums;
+    if (est < best) best = est, p->shape = t.id;
+  }
+  // 64 x 64 tiles with the contraction split over more workgroups and the sums
+  // joined by a second launch: for long contractions of few tiles
+  const int64_t tiles = ceil_div(p->M, 64) * ceil_div(p->N, 64);
+  for (int64_t splits = 2; splits <= 32 && splits <= stages / 2 && tiles * splits <= 3 * kTargetBlocks; splits *= 2) {
+    const int64_t per = ceil_div(stages, splits);
+    const double one = std::max(0.28, 0.26 * static_cast<double>(tiles * splits) / kTargetBlocks);
+    const double est = 2 * kLaunch + kJoin + static_cast<double>(per) * one + static_cast<double>(splits) * m * n * 2e-6;
+    if (est < best) {
+      best = est, p->shape = kProject64;
+      p->k_split = per * 128;
+      p->splits = static_cast<int>(ceil_div(p->K, p->k_split));
+    }
+  }
+}
+
 fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p) {
   if (!s) return set_error(FKL_EINVAL, "shape is NULL");
   if (s->M < 0) return set_error(FKL_EINVAL, "M must be >= 0");
@@ -103,6 +166,10 @@ fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p) {
   if (s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * 4);
   p->off_b = off;
   if (p->b_copied) off = align256(off + static_cast<size_t>(s->N) * row);
+  choose_project_shape(p);
+  p->off_sums = off;
+  if (p->splits > 1)
+    off = align256(off + static_cast<size_t>(p->splits) * s->M * static_cast<size_t>(round_up(s->N, 4)) * 4);
   p->bytes = off;
   return FKL_OK;
 }

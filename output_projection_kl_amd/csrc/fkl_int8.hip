@@ -2,7 +2,7 @@
 // (fkl_quantize), and out = a_scale b_scale (A B^T) + bias over int8 operands
 // (fkl_project), A [M,K] and B [N,K] with k contiguous.
 #include <algorithm>
-#include <cstdlib>
+#include <type_traits>
 
 #include "fkl_decode.h"
 #include "fkl_device.h"
@@ -255,11 +255,14 @@ __global__ __launch_bounds__(256) void k_copy_rows(const int8_t* __restrict__ sr
 struct ProjectParams {
   Operand A, B;  // rows of int8 seen as 16-bit pairs: ld and k_lim count pairs
   int32_t K;
-  int32_t nk;  // contraction stages of 64 bytes
   const float *a_scale, *b_scale, *bias;
   void* out;
   int64_t ldo, M, N;
   int32_t mblocks, nblocks;
+  // Split contraction: split s covers the stages of k_split bytes from s k_split
+  // on, and leaves its sums (T = int32_t) at out + s split_out.
+  int32_t splits, k_split;
+  int64_t split_out;
   DebugCheck dbg;  // debug build: span 0 = out, 1 = A, 2 = B, 3 = a_scale, 4 = b_scale, 5 = bias
 };
 
@@ -267,7 +270,16 @@ struct ProjectParams {
 // conversion), then one fused multiply-add, rounded to the output type.
 template <class T>
 __device__ __forceinline__ T scaled(int32_t sum, float sa, float sb, float bias) {
-  return static_cast<T>(fmaf(static_cast<float>(sum) * sa, sb, bias));
+  float v = fmaf(static_cast<float>(sum) * sa, sb, bias);
+  // the fp32 result stands by itself: the compiler may otherwise round to fp16
+  // within the multiply-add in some of the kernels, and they would differ
+  asm("" : "+v"(v));
+  return static_cast<T>(v);
+}
+
+template <>
+__device__ __forceinline__ int32_t scaled<int32_t>(int32_t sum, float, float, float) {
+  return sum;
 }
 
 // Bytes `valid` .. of a lane's 16 cleared.
@@ -280,25 +292,26 @@ __device__ __forceinline__ i32x4 keep_bytes(i32x4 v, int valid) {
   return v;
 }
 
-// ---- few rows -------------------------------------------------------------
+// ---- few output elements ---------------------------------------------------
 //
-// 16 MB rows of A against 16 columns of the output (rows of B) at a time, the
+// 16 rows of A against 16 columns of the output (rows of B) at a time, the
 // contraction split over the workgroup's 8 waves: wave w takes the F 64-byte
-// fragments from w F on of each span of 512 F bytes. B goes from memory
+// fragments from w F on of each span of 512 F bytes. A and B go from memory
 // straight to the MFMA operands (lane l: row l & 15, 16 bytes at 16 (l >> 4)),
-// the next tile's while this one's are used; A's fragments stay in registers
-// where one span covers K. The waves' partial sums meet in LDS. HBM bound: B
-// is read once, at 8 F KiB per wave in flight.
+// the next tile's B while this one's is used; A's fragments stay in registers
+// where one span covers K. The waves' partial sums meet in LDS. Latency bound:
+// all of a tile's reads are on their way at once, where a block tile goes
+// through its contraction stage by stage (5 x 1024 x 1024: 3 against 5 us).
 constexpr int kSkinnyWaves = 8;
 constexpr int kSkinnyThreads = 64 * kSkinnyWaves;
 
-template <class T, int MB, int F>
-__global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_project_skinny(ProjectParams P, int spans) {
-  __shared__ i32x4 part[2][kSkinnyWaves][MB][64];
+template <class T, int F>
+__global__ __launch_bounds__(kSkinnyThreads) void k_project_skinny(ProjectParams P, int spans) {
+  __shared__ i32x4 part[2][kSkinnyWaves][64];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MB);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 16;
   const int8_t* const a = reinterpret_cast<const int8_t*>(P.A.base);
   const int8_t* const b = reinterpret_cast<const int8_t*>(P.B.base);
   const int64_t lda = P.A.ld * 2, ldb = P.B.ld * 2;
@@ -307,19 +320,15 @@ __global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_projec
 
   // A's bytes past K and rows past M are zero; what is read for B there then
   // does not matter, and comes from inside B.
-  i32x4 fa[MB][F];
+  i32x4 fa[F];
+  const int64_t m_lane = m0 + (lane & 15);
+  const int8_t* const a_row = a + (m_lane < P.M ? m_lane : 0) * lda;
   auto load_a = [&](int span) {
 #pragma unroll
-    for (int x = 0; x < MB; ++x) {
-      const int64_t m = m0 + x * 16 + (lane & 15);
-#pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int k = span * (kSkinnyWaves * F * 64) + k_lane + f * 64;
-        fa[x][f] = i32x4{0, 0, 0, 0};
-        if (m < P.M && k < P.K)
-          fa[x][f] = keep_bytes(dload(P.dbg, 1, kDbgProjectOperand, reinterpret_cast<const i32x4*>(a + m * lda + k)),
-                                P.K - k);
-      }
+    for (int f = 0; f < F; ++f) {
+      const int k = span * (kSkinnyWaves * F * 64) + k_lane + f * 64;
+      const i32x4 v = dload(P.dbg, 1, kDbgProjectOperand, reinterpret_cast<const i32x4*>(a_row + (k < K16 ? k : 0)));
+      fa[f] = keep_bytes(v, m_lane < P.M ? P.K - k : 0);
     }
   };
   auto load_b = [&](int tile, int span, i32x4 (&fb)[F]) {
@@ -332,35 +341,26 @@ __global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_projec
       fb[f] = dload(P.dbg, 2, kDbgProjectOperand, reinterpret_cast<const i32x4*>(row + (k < K16 ? k : 0)));
     }
   };
-  i32x4 acc[MB];
+  i32x4 acc;
   auto mma = [&](const i32x4 (&fb)[F]) {
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-      for (int x = 0; x < MB; ++x) acc[x] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[x][f], fb[f], acc[x], 0, 0, 0);
+    for (int f = 0; f < F; ++f) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[f], fb[f], acc, 0, 0, 0);
   };
-  // The tile's sums: element e of 16 MB x 16 from the waves' accumulators
-  // (lane l of wave w: column l & 15, rows 4 (l >> 4) .. + 3 of each block).
+  // The tile's sums from the waves' accumulators (lane l: column l & 15, rows 4 (l >> 4) .. + 3).
   auto finish = [&](int tile, int turn) {
-#pragma unroll
-    for (int x = 0; x < MB; ++x) part[turn][wave][x][lane] = acc[x];
+    part[turn][wave][lane] = acc;
     __syncthreads();
-    constexpr int kElems = MB * 256;
+    const int row = tid >> 4, col = tid & 15;
+    const int64_t m = m0 + row, n = static_cast<int64_t>(tile) * 16 + col;
+    if (tid < 256 && m < P.M && n < P.N) {
+      int32_t sum = 0;
 #pragma unroll
-    for (int e0 = 0; e0 < kElems; e0 += kSkinnyThreads) {
-      const int e = e0 + tid;
-      const int row = e >> 4, col = e & 15;
-      const int64_t m = m0 + row, n = static_cast<int64_t>(tile) * 16 + col;
-      if (e < kElems && m < P.M && n < P.N) {
-        const int l = ((row & 15) >> 2) * 16 + col;
-        int32_t sum = 0;
-#pragma unroll
-        for (int w = 0; w < kSkinnyWaves; ++w) sum += reinterpret_cast<const int32_t*>(&part[turn][w][row >> 4][l])[row & 3];
-        const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m);
-        const float sb = dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n);
-        const float bias = P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n) : 0.0f;
-        dstore(P.dbg, 0, kDbgProjectOut, static_cast<T*>(P.out) + m * P.ldo + n, scaled<T>(sum, sa, sb, bias));
-      }
+      for (int w = 0; w < kSkinnyWaves; ++w)
+        sum += reinterpret_cast<const int32_t*>(&part[turn][w][(row >> 2) * 16 + col])[row & 3];
+      const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m);
+      const float sb = dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n);
+      const float bias = P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n) : 0.0f;
+      dstore(P.dbg, 0, kDbgProjectOut, static_cast<T*>(P.out) + m * P.ldo + n, scaled<T>(sum, sa, sb, bias));
     }
   };
 
@@ -375,8 +375,7 @@ __global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_projec
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (tile + step < P.nblocks) load_b(tile + step, 0, fb[1 - h]);
-#pragma unroll
-        for (int x = 0; x < MB; ++x) acc[x] = i32x4{0, 0, 0, 0};
+        acc = i32x4{0, 0, 0, 0};
         mma(fb[h]);
         finish(tile, h);
         tile += step;
@@ -385,8 +384,7 @@ __global__ __launch_bounds__(kSkinnyThreads, MB * F <= 16 ? 4 : 2) void k_projec
     }
   }
   for (int tile = blockIdx.x; tile < P.nblocks; tile += step, turn ^= 1) {
-#pragma unroll
-    for (int x = 0; x < MB; ++x) acc[x] = i32x4{0, 0, 0, 0};
+    acc = i32x4{0, 0, 0, 0};
     for (int span = 0; span < spans; ++span) {
       i32x4 fb[F];
       load_b(tile, span, fb);
@@ -600,17 +598,21 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
   const int lane = tid & 63;
   const int wave = tid >> 6;
   int mbi, nbi;
-  grouped_tile(xcd_contiguous(blockIdx.x, P.mblocks * P.nblocks), P.mblocks, P.nblocks, 8, mbi, nbi);
+  const int tiles = P.mblocks * P.nblocks;
+  const int at = xcd_contiguous(blockIdx.x, tiles * P.splits);
+  const int split = at / tiles;
+  grouped_tile(at - split * tiles, P.mblocks, P.nblocks, 8, mbi, nbi);
   const int64_t m0 = static_cast<int64_t>(mbi) * C::TM;
   const int64_t n0 = static_cast<int64_t>(nbi) * C::TN;
+  const int k0 = split * P.k_split;
+  const Operand A = k_window<false>(P.A, k0 / 2, P.k_split / 2);
+  const Operand B = k_window<false>(P.B, k0 / 2, P.k_split / 2);
   i32x4 acc[C::XA][C::XB];
-  dcheck_operand(P.dbg, 1, P.A, m0, C::TM, false);
-  dcheck_operand(P.dbg, 2, P.B, n0, C::TN, false);
-  int8_mainloop<C>(P.A, P.B, m0, n0, P.K, acc, lds);
+  dcheck_operand(P.dbg, 1, A, m0, C::TM, false);
+  dcheck_operand(P.dbg, 2, B, n0, C::TN, false);
+  int8_mainloop<C>(A, B, m0, n0, min(P.K - k0, P.k_split), acc, lds);
   constexpr int kCols = C::out_cols(sizeof(T));
   constexpr int kPitch = C::out_pitch(sizeof(T));
-  constexpr int kPer = 16 / sizeof(T);     // elements of a 16-byte piece
-  constexpr int kLanes = kCols / kPer;     // pieces of a staged row
   typedef T T4 __attribute__((ext_vector_type(4)));
   const int m_wave = (wave / C::WN) * (C::XA * 16) + (lane & 15);  // of this lane's rows within the tile
   const int n_wave = (wave % C::WN) * (C::XB * 16) + 4 * (lane >> 4);
@@ -618,10 +620,9 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
 #pragma unroll
   for (int x = 0; x < C::XA; ++x) {
     const int64_t m = m0 + m_wave + x * 16;
-    sa[x] = m < P.M ? dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m) : 0.0f;
+    sa[x] = std::is_same<T, int32_t>::value || m >= P.M ? 0.0f : dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m);
   }
-  T* const out = static_cast<T*>(P.out) + m0 * P.ldo + n0;
-  const bool whole = P.ldo % kPer == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0;
+  T* const out = static_cast<T*>(P.out) + split * P.split_out + m0 * P.ldo + n0;
   const int rmax = static_cast<int>(min<int64_t>(C::TM, P.M - m0));
 #pragma unroll
   for (int c0 = 0; c0 < C::TN; c0 += kCols) {
@@ -634,7 +635,7 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
       float sb[4], bias[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = col + j < cmax;
+        const bool in = !std::is_same<T, int32_t>::value && col + j < cmax;
         sb[j] = in ? dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n0 + c0 + col + j) : 0.0f;
         bias[j] = in && P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n0 + c0 + col + j) : 0.0f;
       }
@@ -645,26 +646,65 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
                scaled<T>(acc[x][y][2], sa[x], sb[2], bias[2]), scaled<T>(acc[x][y][3], sa[x], sb[3], bias[3])};
     }
     __syncthreads();
-    if (whole) {
-      const int c = (tid % kLanes) * kPer;
-      for (int r = tid / kLanes; r < rmax; r += C::kThreads / kLanes) {
-        const char* const from = lds + r * kPitch + c * static_cast<int>(sizeof(T));
-        T* const to = out + r * P.ldo + c0 + c;
-        if (c + kPer <= cmax) {
-          dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<u32x4*>(to), *reinterpret_cast<const u32x4*>(from));
+    // 16 bytes of a row per lane, at 16-byte boundaries of the output: the
+    // staged row is read `mis` bytes before the piece's own start where rows do
+    // not start at such a boundary, in words, shifted by half a word if need be.
+    constexpr int kSize = static_cast<int>(sizeof(T));
+    constexpr int kPieces = kCols * kSize / 16;
+    auto store_rows = [&](auto at_boundary) {
+      constexpr int kAcross = kPieces + (at_boundary ? 0 : 1);
+      constexpr int kDown = C::kThreads / kAcross;
+      const int b = (tid % kAcross) * 16;
+      for (int r = tid / kAcross; r < rmax && tid < kAcross * kDown; r += kDown) {
+        char* const row = reinterpret_cast<char*>(out + r * P.ldo + c0);
+        const int mis = at_boundary ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        const int b0 = b - mis;  // the piece's first byte in the row
+        const char* const from = lds + r * kPitch;
+        if (b0 >= 0 && b0 + 16 <= cmax * kSize) {
+          u32x4 v;
+          if (mis == 0) {
+            v = *reinterpret_cast<const u32x4*>(from + b0);
+          } else {
+            const uint32_t* const w = reinterpret_cast<const uint32_t*>(from + (b0 & ~3));
+            v = u32x4{w[0], w[1], w[2], w[3]};
+            if (kSize == 2 && (b0 & 2)) {
+              const uint32_t next = w[4];
+              v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16 | next << 16};
+            }
+          }
+          dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<u32x4*>(row + b0), v);
         } else {
-          for (int j = 0; c + j < cmax; ++j)
-            dstore(P.dbg, 0, kDbgProjectOut, to + j, reinterpret_cast<const T*>(from)[j]);
+          for (int e = max(b0, 0); e < min(b0 + 16, cmax * kSize); e += kSize)
+            dstore(P.dbg, 0, kDbgProjectOut, reinterpret_cast<T*>(row + e), *reinterpret_cast<const T*>(from + e));
         }
       }
-    } else {  // rows that do not start at 16 bytes: neighbouring lanes on neighbouring elements
-      constexpr int kAcross = kCols < C::kThreads ? kCols : C::kThreads;
-      for (int r = tid / kAcross; r < rmax; r += C::kThreads / kAcross)
-        for (int c = tid % kAcross; c < cmax; c += kAcross)
-          dstore(P.dbg, 0, kDbgProjectOut, out + r * P.ldo + c0 + c,
-                 reinterpret_cast<const T*>(lds + r * kPitch)[c]);
-    }
+    };
+    if (P.ldo * kSize % 16 == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0)
+      store_rows(std::integral_constant<bool, true>());
+    else
+      store_rows(std::integral_constant<bool, false>());
     if (c0 + kCols < C::TN) __syncthreads();
+  }
+}
+
+// The sums of a split contraction added up, scaled and rounded.
+template <class T>
+__global__ __launch_bounds__(256) void k_project_join(ProjectParams P, const int32_t* __restrict__ sums, int64_t ld) {
+  const int64_t quads = (P.N + 3) / 4;
+  const int64_t total = P.M * quads;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t m = i / quads;
+    const int64_t n = (i - m * quads) * 4;
+    i32x4 sum{0, 0, 0, 0};
+    for (int s = 0; s < P.splits; ++s) sum += *reinterpret_cast<const i32x4*>(sums + s * P.split_out + m * ld + n);
+    const float sa = dload(P.dbg, 3, kDbgProjectOperand, P.a_scale + m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j >= P.N) break;
+      const float sb = dload(P.dbg, 4, kDbgProjectOperand, P.b_scale + n + j);
+      const float bias = P.bias ? dload(P.dbg, 5, kDbgProjectOperand, P.bias + n + j) : 0.0f;
+      dstore(P.dbg, 0, kDbgProjectOut, static_cast<T*>(P.out) + m * P.ldo + n + j, scaled<T>(sum[j], sa, sb, bias));
+    }
   }
 }
 
@@ -672,61 +712,67 @@ using Tile256 = IntTile<256, 256, 2, 4, 2>;
 using Tile256x128 = IntTile<256, 128, 4, 2, 3>;
 using Tile128x256 = IntTile<128, 256, 2, 4, 3>;
 using Tile128 = IntTile<128, 128, 2, 2, 2>;
-using Tile128s4 = IntTile<128, 128, 2, 2, 4>;
-using Tile64 = IntTile<64, 64, 2, 2, 3>;
 using Tile64x128 = IntTile<64, 128, 2, 2, 3>;
-using Tile32x128 = IntTile<32, 128, 1, 4, 3>;
-using Tile16x128 = IntTile<16, 128, 1, 4, 4>;
+using Tile64 = IntTile<64, 64, 2, 2, 3>;
 using Tile16x64 = IntTile<16, 64, 1, 4, 4>;
 
 template <class T, class C>
 static void launch_tiles(ProjectParams P, hipStream_t st) {
   P.mblocks = static_cast<int32_t>(ceil_div(P.M, C::TM));
   P.nblocks = static_cast<int32_t>(ceil_div(P.N, C::TN));
-  hipLaunchKernelGGL((k_project<T, C>), dim3(static_cast<unsigned>(P.mblocks) * P.nblocks), dim3(C::kThreads), 0, st,
-                     P);
+  hipLaunchKernelGGL((k_project<T, C>), dim3(static_cast<unsigned>(P.mblocks) * P.nblocks * P.splits),
+                     dim3(C::kThreads), 0, st, P);
 }
 
-template <class T, int MB>
+template <class T>
 static void launch_skinny(ProjectParams P, hipStream_t st) {
   P.nblocks = static_cast<int32_t>(ceil_div(P.N, 16));
-  P.mblocks = static_cast<int32_t>(ceil_div(P.M, 16 * MB));
-  const int per_wave = static_cast<int>(ceil_div(P.nk, kSkinnyWaves));
+  P.mblocks = static_cast<int32_t>(ceil_div(P.M, 16));
+  const int per_wave = static_cast<int>(ceil_div(P.K, 64 * kSkinnyWaves));
   // as many workgroups as fit on the CUs at once, in all
   const int resident = 2 * kTargetBlocks;
   const dim3 grid(static_cast<unsigned>(std::min(P.nblocks, std::max(1, resident / P.mblocks))),
                   static_cast<unsigned>(P.mblocks));
   const dim3 block(kSkinnyThreads);
-  if (per_wave <= 2) hipLaunchKernelGGL((k_project_skinny<T, MB, 2>), grid, block, 0, st, P, 1);
-  else if (per_wave <= 4) hipLaunchKernelGGL((k_project_skinny<T, MB, 4>), grid, block, 0, st, P, 1);
+  if (per_wave <= 2) hipLaunchKernelGGL((k_project_skinny<T, 2>), grid, block, 0, st, P, 1);
+  else if (per_wave <= 4) hipLaunchKernelGGL((k_project_skinny<T, 4>), grid, block, 0, st, P, 1);
   else
-    hipLaunchKernelGGL((k_project_skinny<T, MB, 8>), grid, block, 0, st, P,
-                       static_cast<int>(ceil_div(P.nk, 8 * kSkinnyWaves)));
-}
-
-static int forced_variant() {
-  const char* v = std::getenv("FKL_VARIANT");
-  return v ? std::atoi(v) : 0;
+    hipLaunchKernelGGL((k_project_skinny<T, 8>), grid, block, 0, st, P, static_cast<int>(ceil_div(per_wave, 8)));
 }
 
 template <class T>
-static void launch_product(const ProjectParams& P, hipStream_t st) {
-  const int v = forced_variant();
-  if (v ? v == 1 : P.M <= 16) return launch_skinny<T, 1>(P, st);
-  if (v ? v == 2 : P.M <= 32) return launch_skinny<T, 2>(P, st);
-  if (v ? v == 3 : P.M <= 64) return launch_skinny<T, 4>(P, st);
-  if (v == 7) return launch_tiles<T, Tile64>(P, st);
-  if (v == 8) return launch_tiles<T, Tile128s4>(P, st);
-  if (v == 10) return launch_tiles<T, Tile128x256>(P, st);
-  if (v == 11) return launch_tiles<T, Tile64x128>(P, st);
-  if (v == 12) return launch_tiles<T, Tile32x128>(P, st);
-  if (v == 13) return launch_tiles<T, Tile16x128>(P, st);
-  if (v == 14) return launch_tiles<T, Tile16x64>(P, st);
-  auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(P.M, tm) * ceil_div(P.N, tn); };
-  if (v ? v == 4 : tiles(256, 256) >= kTargetBlocks) return launch_tiles<T, Tile256>(P, st);
-  if (v ? v == 5 : tiles(256, 128) >= kTargetBlocks) return launch_tiles<T, Tile256x128>(P, st);
-  if (v ? v == 6 : tiles(128, 128) >= kTargetBlocks) return launch_tiles<T, Tile128>(P, st);
-  launch_tiles<T, Tile64>(P, st);
+static void launch_shape(ProjectShapeId id, const ProjectParams& P, hipStream_t st) {
+  switch (id) {
+    case kProjectSkinny: return launch_skinny<T>(P, st);
+    case kProject16x64: return launch_tiles<T, Tile16x64>(P, st);
+    case kProject64: return launch_tiles<T, Tile64>(P, st);
+    case kProject64x128: return launch_tiles<T, Tile64x128>(P, st);
+    case kProject128: return launch_tiles<T, Tile128>(P, st);
+    case kProject128x256: return launch_tiles<T, Tile128x256>(P, st);
+    case kProject256x128: return launch_tiles<T, Tile256x128>(P, st);
+    case kProject256: return launch_tiles<T, Tile256>(P, st);
+  }
+}
+
+template <class T>
+static void launch_product(const ProjectPlan& p, ProjectParams P, char* ws, hipStream_t st) {
+  if (p.splits == 1) return launch_shape<T>(p.shape, P, st);
+  // sums of each split, then their join; only the 64 x 64 tiles are split
+  ProjectParams Q = P;
+  int32_t* const sums = reinterpret_cast<int32_t*>(ws + p.off_sums);
+  const int64_t ld = round_up(p.N, 4);
+  Q.out = sums;
+  Q.ldo = ld;
+  P.splits = Q.splits = p.splits;
+  P.split_out = Q.split_out = p.M * ld;
+  Q.k_split = static_cast<int32_t>(p.k_split);
+  Q.dbg = P.dbg;
+#ifdef FKL_DEBUG
+  Q.dbg.s[0] = DebugSpan{reinterpret_cast<const char*>(sums), static_cast<uint64_t>(p.splits) * p.M * ld * 4};
+#endif
+  launch_tiles<int32_t, Tile64>(Q, st);
+  const int64_t grid = std::min<int64_t>(ceil_div(p.M * (ld / 4), 256), 4096);
+  hipLaunchKernelGGL(k_project_join<T>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, P, sums, ld);
 }
 
 hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_t st) {
@@ -763,7 +809,9 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   P.A = Operand{reinterpret_cast<const uint16_t*>(a), lda / 2, p.M, row16 / 2};
   P.B = Operand{reinterpret_cast<const uint16_t*>(b), ldb / 2, p.N, row16 / 2};
   P.K = static_cast<int32_t>(p.K);
-  P.nk = static_cast<int32_t>(ceil_div(p.K, 64));
+  P.splits = 1;
+  P.k_split = static_cast<int32_t>(round_up(p.K, kIntStageK));
+  P.split_out = 0;
   P.a_scale = a_scale, P.b_scale = g.b_scale, P.bias = g.bias;
   P.out = g.out;
   P.ldo = p.ldo, P.M = p.M, P.N = p.N;
@@ -778,10 +826,12 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   const double flops = 2.0 * p.M * static_cast<double>(p.N) * p.K;
   const double bytes = static_cast<double>(p.M) * p.K + static_cast<double>(p.N) * p.K +
                        static_cast<double>(p.M) * p.N * type_bytes(p.out_type);
-  TraceScope ts(st, "project", flops, bytes);
-  if (p.out_type == FKL_F32) launch_product<float>(P, st);
-  else if (p.out_type == FKL_BF16) launch_product<__bf16>(P, st);
-  else launch_product<_Float16>(P, st);
+  static const char* const kNames[] = {"project_16x16",   "project_16x64",   "project_64x64",   "project_64x128",
+                                       "project_128x128", "project_128x256", "project_256x128", "project_256x256"};
+  TraceScope ts(st, p.splits > 1 ? "project_split" : kNames[p.shape], flops, bytes);
+  if (p.out_type == FKL_F32) launch_product<float>(p, P, g.ws, st);
+  else if (p.out_type == FKL_BF16) launch_product<__bf16>(p, P, g.ws, st);
+  else launch_product<_Float16>(p, P, g.ws, st);
   return hipGetLastError();
 }
 

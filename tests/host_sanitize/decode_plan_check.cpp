@@ -51,6 +51,12 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& a, hipStream_
   if (p.a_type != FKL_I8) end = p.off_a_scale + p.M * 4;
   CHECK(p.off_b >= end && p.off_b % 256 == 0);
   if (p.b_copied) end = p.off_b + p.N * row;
+  CHECK(p.off_sums >= end && p.off_sums % 256 == 0);
+  CHECK(p.splits >= 1 && p.splits <= 32 && p.splits * p.k_split >= p.K);
+  if (p.splits > 1) {  // every split has something to add up, in whole stages
+    CHECK(p.shape == kProject64 && p.k_split % 128 == 0 && (p.splits - 1) * p.k_split < p.K);
+    end = p.off_sums + static_cast<size_t>(p.splits) * p.M * round_up(p.N, 4) * 4;
+  }
   CHECK(p.bytes >= end);
   if (p.a_type == FKL_I8 && !p.a_copied) CHECK(p.lda % 16 == 0 && kTile * p.lda <= INT32_MAX);
   if (!p.b_copied) CHECK(p.ldb % 16 == 0 && kTile * p.ldb <= INT32_MAX);

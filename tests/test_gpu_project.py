@@ -130,6 +130,42 @@ def test_project_int8_rows(M, N, K, out):
     _check_product(got, a, sa, b, sb, bias)
 
 
+# One size and more for every layout of the product, under the names of the
+# library's trace; ragged in every dimension.
+LAYOUTS = [(5, 70, 500, "project_16x16"), (85, 706, 417, "project_16x16"), (9, 30001, 1000, "project_16x64"),
+           (60, 40001, 1030, "project_64x64"), (38, 56217, 335, "project_64x128"), (117, 31149, 1090, "project_128x128"),
+           (139, 19627, 2383, "project_128x256"), (201, 32003, 2887, "project_256x128"),
+           (1030, 20003, 700, "project_256x256"), (505, 323, 7071, "project_split"), (3, 16, 9000, "project_split"),
+           (100, 65, 20011, "project_split")]
+
+
+@pytest.mark.parametrize("M,N,K,layout", LAYOUTS)
+def test_project_every_layout(M, N, K, layout):
+    dev = _dev()
+    g = torch.Generator(device=dev).manual_seed(M + N + K)
+    a = torch.randint(-128, 128, (M, -(-K // 16) * 16), generator=g, dtype=torch.int8, device=dev)[:, :K]
+    b = torch.randint(-128, 128, (N, -(-K // 16) * 16), generator=g, dtype=torch.int8, device=dev)[:, :K]
+    sa = (torch.rand(M, generator=g, device=dev) + 0.5) / 127
+    sb = (torch.rand(N, generator=g, device=dev) + 0.5) / (127 * K ** 0.5)
+    bias = torch.randn(N, generator=g, device=dev)
+    print(f"[project] {layout} M={M} N={N} K={K}", flush=True)
+    fkl.trace_read()
+    fkl.trace_enable(True)
+    half = fkl.project(a, b, sb, a_scale=sa, bias=bias, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    fkl.trace_enable(False)
+    assert [k["name"] for k in fkl.trace_read()] == [layout]
+    outs = [half] + [fkl.project(a, b, sb, a_scale=sa, bias=bias, out_dtype=t) for t in TYPES]
+    torch.cuda.synchronize()
+    # fp64 products of int8 sums are exact; the oracle's steps on the GPU
+    prod = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+    want = prod + bias.double()
+    for out in outs:
+        tol = 1.01 * (2 * 2.0 ** -24 * prod.abs() + (2.0 ** -24 + torch.finfo(out.dtype).eps / 2) * want.abs()) + 2.0 ** -25
+        assert ((out.double() - want).abs() <= tol).all(), out.dtype
+    assert torch.equal(half, outs[1 + TYPES.index(torch.bfloat16)])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,N,K", [(1, 300, 2880), (1, 17, 3), (7, 129, 1000), (40, 257, 72), (130, 200, 2887), (300, 300, 64)])
 def test_project_floating_rows_are_quantised_first(M, N, K, dtype):
