@@ -431,8 +431,9 @@ typedef struct {
 
 /*
  * Workspace bytes of fkl_project for this shape (host only; bytes may be
- * NULL): room for quantised rows of a and for copies of operands that are not
- * read where they are.
+ * NULL): room for quantised rows of a, for copies of operands that are not
+ * read where they are, and for the parts of a long sum where the output is
+ * small. 0 where none of these is needed; the workspace may then be NULL.
  * Errors: those of fkl_project that the shape alone decides.
  */
 fkl_status fkl_project_workspace_size(const fkl_project_shape* shape, size_t* bytes);
@@ -491,7 +492,9 @@ typedef struct {
 } fkl_sample_params;
 
 /* Workspace bytes of fkl_sample for this shape (host only; bytes may be
- * NULL). Errors: those of fkl_sample that the shape alone decides. */
+ * NULL): statistics of each row where V is above 1024, about 5 KiB for every
+ * 4096 entries (16384 with many rows). 0 for shorter rows; the workspace may
+ * then be NULL. Errors: those of fkl_sample that the shape alone decides. */
 fkl_status fkl_sample_workspace_size(const fkl_sample_shape* shape, size_t* bytes);
 
 fkl_status fkl_sample(const fkl_sample_shape* shape, const fkl_sample_params* params, const void* logits,

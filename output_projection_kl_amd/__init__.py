@@ -738,9 +738,9 @@ def project(a, b, b_scale, a_scale=None, bias=None, out_dtype=None, out=None, wo
     s = ctypes.byref(ProjectShape(M, N, K, lda, ldb, ldo, code, _type_of(out, "out"), flags))
     L, need = lib(), ctypes.c_size_t(0)
     _check(L.fkl_project_workspace_size(s, ctypes.byref(need)))
-    ws = _workspace(need.value, dev, workspace)
+    ws = _workspace(need.value, dev, workspace) if need.value else None
     _enqueue(dev, L.fkl_project, s, a.data_ptr(), None if a_scale is None else a_scale.data_ptr(), b.data_ptr(),
-             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), ws.data_ptr(), _nbytes(ws))
+             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(), need.value)
     return out
 
 
@@ -796,9 +796,9 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, 
     params = SampleParams(T_rows, k_rows, p_rows, q_rows, T, max(-1, min(int(k), V)), p, q)
     L, need = lib(), ctypes.c_size_t(0)
     _check(L.fkl_sample_workspace_size(s, ctypes.byref(need)))
-    ws = _workspace(need.value, dev, workspace)
+    ws = _workspace(need.value, dev, workspace) if need.value else None
     _enqueue(dev, L.fkl_sample, s, ctypes.byref(params), logits.data_ptr(), None if ids is None else ids.data_ptr(),
-             u.data_ptr(), token.data_ptr(), logprob.data_ptr(), ws.data_ptr(), _nbytes(ws))
+             u.data_ptr(), token.data_ptr(), logprob.data_ptr(), None if ws is None else ws.data_ptr(), need.value)
     return token, logprob
 
 

@@ -22,7 +22,15 @@ bool readable_stride(int64_t ld) { return ld % 16 == 0 && ld <= (int64_t(1) << 2
 
 bool is_float_type(int t) { return t == FKL_F32 || t == FKL_BF16 || t == FKL_F16; }
 
+// The debug build keeps its violation word at the start of every workspace.
+#ifdef FKL_DEBUG
+constexpr size_t kControlBytes = 256;
+#else
+constexpr size_t kControlBytes = 0;
+#endif
+
 fkl_status check_workspace(const void* workspace, size_t given, size_t need, const char* size_call) {
+  if (need == 0) return FKL_OK;
   if (!workspace) return set_error(FKL_EWORKSPACE, "workspace is NULL");
   if (!aligned(workspace, 256)) return set_error(FKL_EWORKSPACE, "workspace must be 256-byte aligned");
   if (given < need) return set_error(FKL_EWORKSPACE, std::string("workspace is smaller than ") + size_call);
@@ -159,7 +167,7 @@ fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p) {
   p->a_copied = s->a_type == FKL_I8 && ((s->flags & FKL_PROJECT_COPY_A) || !readable_stride(s->lda));
   p->b_copied = (s->flags & FKL_PROJECT_COPY_B) || !readable_stride(s->ldb);
   const size_t row = static_cast<size_t>(round_up(s->K, 16));
-  size_t off = 256;
+  size_t off = kControlBytes;
   p->off_a = off;
   if (p->a_copied || s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * row);
   p->off_a_scale = off;
@@ -189,7 +197,7 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   p->type = s->type;
   p->route = s->V <= kSampleShortMaxV ? kSampleShort : s->V <= kSampleScanMaxV ? kSampleScan : kSampleLong;
   p->groups = p->chunks = p->chunk_elems = p->group_shift = 0;
-  size_t off = 256;
+  size_t off = kControlBytes;
   p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
   if (p->route == kSampleScan) {
     // the larger chunks where they leave enough workgroups for every CU

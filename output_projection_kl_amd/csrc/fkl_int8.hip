@@ -134,8 +134,9 @@ __device__ __forceinline__ void pack_levels(const typename QuantOf<T>::Scale& s,
   }
 }
 
-// One workgroup per row, rows of whole 16-byte pieces (x 16-byte aligned, cols
-// a multiple of 16 / sizeof(T), q aligned to the piece's levels).
+// One workgroup per row, in pieces of 16 bytes of x; the row's last few
+// elements one by one. Pieces are read and written at any alignment (the GPU
+// splits an access that crosses a line).
 template <class T>
 __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict__ x, int64_t ldx, int cols,
                                                             int8_t* __restrict__ q, int64_t ldq,
@@ -143,23 +144,39 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict_
   __shared__ uint32_t shared[kQuantThreads / 64];
   constexpr int kPer = 16 / sizeof(T);
   constexpr int kHeld = kQuantHeldBytes / 16;
+  constexpr int kWords = kPer / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  struct __attribute__((packed)) AnyPiece {
+    u32x4 v;
+  };
+  struct __attribute__((packed)) AnyWords {
+    Words v;
+  };
   const int64_t row = blockIdx.x;
-  const u32x4* src = reinterpret_cast<const u32x4*>(x + row * ldx);
-  int8_t* dst = q + row * ldq;
+  const T* const src = x + row * ldx;
+  int8_t* const dst = q + row * ldq;
   const int n = cols / kPer;
+  const int tail = n * kPer + threadIdx.x;  // this thread's element of the tail
+  auto get = [&](int i) { return reinterpret_cast<const AnyPiece*>(src + static_cast<int64_t>(i) * kPer)->v; };
+  auto element = [&](int i) -> uint32_t {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(uint32_t, src[i]);
+    else return __builtin_bit_cast(uint16_t, src[i]);
+  };
   u32x4 held[kHeld];
   uint32_t m = 0;
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
     const int i = threadIdx.x + h * kQuantThreads;
-    held[h] = i < n ? src[i] : u32x4{0, 0, 0, 0};
+    held[h] = i < n ? get(i) : u32x4{0, 0, 0, 0};
   }
+  const uint32_t last = tail < cols ? element(tail) : 0u;
 #pragma unroll
   for (int h = 0; h < kHeld; ++h)
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = QuantOf<T>::wider(m, held[h][j]);
+  m = QuantOf<T>::wider(m, last);
   for (int i = threadIdx.x + kHeld * kQuantThreads; i < n; i += kQuantThreads) {
-    const u32x4 v = src[i];
+    const u32x4 v = get(i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = QuantOf<T>::wider(m, v[j]);
   }
@@ -167,56 +184,31 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict_
   if (threadIdx.x == 0) scale[row] = row_scale<T>(mag);
   const bool zero = mag == 0 || mag >= QuantOf<T>::kInf;
   const typename QuantOf<T>::Scale s(zero ? 1.0f : QuantOf<T>::value(mag));
-  constexpr int kWords = kPer / 4;
-  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
   auto put = [&](int i, u32x4 v) {
     uint32_t w[kWords];
     pack_levels<T>(s, v, w);
-    if constexpr (kWords == 1) *reinterpret_cast<uint32_t*>(dst + i * kPer) = zero ? 0u : w[0];
-    else *reinterpret_cast<u32x2*>(dst + i * kPer) = zero ? u32x2{0, 0} : u32x2{w[0], w[1]};
+    Words out;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) out[j] = zero ? 0u : w[j];
+    reinterpret_cast<AnyWords*>(dst + static_cast<int64_t>(i) * kPer)->v = out;
   };
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
     const int i = threadIdx.x + h * kQuantThreads;
     if (i < n) put(i, held[h]);
   }
-  for (int i = threadIdx.x + kHeld * kQuantThreads; i < n; i += kQuantThreads) put(i, src[i]);
-}
-
-// Any columns, stride and alignment, one element at a time.
-template <class T>
-__global__ __launch_bounds__(kQuantThreads) void k_quantize_any(const T* __restrict__ x, int64_t ldx, int cols,
-                                                                int8_t* __restrict__ q, int64_t ldq,
-                                                                float* __restrict__ scale) {
-  __shared__ uint32_t shared[kQuantThreads / 64];
-  const int64_t row = blockIdx.x;
-  const T* src = x + row * ldx;
-  int8_t* dst = q + row * ldq;
-  auto bits = [&](int i) -> uint32_t {
-    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(uint32_t, src[i]);
-    else return __builtin_bit_cast(uint16_t, src[i]);
-  };
-  uint32_t m = 0;
-  for (int i = threadIdx.x; i < cols; i += kQuantThreads) m = QuantOf<T>::wider(m, bits(i));
-  const uint32_t mag = block_magnitude<T>(m, shared);
-  if (threadIdx.x == 0) scale[row] = row_scale<T>(mag);
-  const bool zero = mag == 0 || mag >= QuantOf<T>::kInf;
-  const typename QuantOf<T>::Scale s(zero ? 1.0f : QuantOf<T>::value(mag));
-  for (int i = threadIdx.x; i < cols; i += kQuantThreads)
-    dst[i] = zero ? int8_t(0) : static_cast<int8_t>(s.level(QuantOf<T>::value(bits(i))));
+  for (int i = threadIdx.x + kHeld * kQuantThreads; i < n; i += kQuantThreads) put(i, get(i));
+  if (tail < cols) dst[tail] = zero ? int8_t(0) : static_cast<int8_t>(s.level(QuantOf<T>::value(last)));
 }
 
 template <class T>
 static void launch_quantize_of(int64_t rows, int64_t cols, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
                                float* scale, hipStream_t st) {
-  constexpr int kPer = 16 / sizeof(T);
-  const bool whole = cols % kPer == 0 && ldx % kPer == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-                     ldq % kPer == 0 && reinterpret_cast<uintptr_t>(q) % kPer == 0;
   constexpr int64_t kRowsPerLaunch = int64_t(1) << 23;  // grid x block stays below 2^32 threads
   for (int64_t r = 0; r < rows; r += kRowsPerLaunch)
-    hipLaunchKernelGGL(whole ? k_quantize<T> : k_quantize_any<T>,
-                       dim3(static_cast<unsigned>(std::min(rows - r, kRowsPerLaunch))), dim3(kQuantThreads), 0, st,
-                       static_cast<const T*>(x) + r * ldx, ldx, static_cast<int>(cols), q + r * ldq, ldq, scale + r);
+    hipLaunchKernelGGL(k_quantize<T>, dim3(static_cast<unsigned>(std::min(rows - r, kRowsPerLaunch))),
+                       dim3(kQuantThreads), 0, st, static_cast<const T*>(x) + r * ldx, ldx, static_cast<int>(cols),
+                       q + r * ldq, ldq, scale + r);
 }
 
 hipError_t launch_quantize(int64_t rows, int64_t cols, int type, const void* x, int64_t ldx, int8_t* q, int64_t ldq,

@@ -1631,7 +1631,7 @@ hipError_t launch_sample(const SamplePlan& p, const SampleArgs& a, hipStream_t s
                             {a.u, n * 4},
                             {a.token, n * 4},
                             {a.logprob, a.logprob ? n * 4 : 0},
-                            {a.ws + 256, p.bytes - 256}});
+                            {a.ws, p.bytes}});
   // V weights of at most 2^shift each stay below 2^63
   int shift = 46;
   while ((p.V >> (62 - shift)) > 0) --shift;
