@@ -143,33 +143,61 @@ __device__ __forceinline__ double exp2_f64(double t) {
   return ldexp(s, static_cast<int>(n));
 }
 
-// 2^(t / 16) split for the scan, which takes one of every entry: t = b + f with
-// b the nearest integer (found by adding and subtracting 1.5 * 2^52, whose sum
-// holds b in its low word; |t| < 2^31) and |f| <= 1/2; 2^(f / 16) by Taylor's
-// series to the 5th power (remainder below 0.0217^6 / 6! = 1.5e-13).
-struct Sixteenths {
+// 2^(t / 8): t = b + f with b the nearest integer (found by adding and
+// subtracting 1.5 * 2^52, whose sum holds b in its low word; |t| < 2^31) and
+// |f| <= 1/2; 2^(f / 8) by Taylor's series to the 6th power (remainder below
+// 0.0434^7 / 7! = 6e-14). The scan takes one of these of every entry: the
+// series' coefficients are kept in scalar registers, which the compiler would
+// otherwise copy to vector registers for each entry (a third more instructions).
+struct Eighths {
   int b;
   double f;
-  __device__ __forceinline__ explicit Sixteenths(double t) {
+  __device__ __forceinline__ explicit Eighths(double t) {
     const double r = t + 6755399441055744.0;
     b = static_cast<int>(__double2loint(r));
     f = t - (r - 6755399441055744.0);
   }
-  __device__ __forceinline__ double fraction() const {
-    constexpr double g = 0.69314718055994530942 / 16.0;
-    double s = fma(g * g * g * g * g / 120.0, f, g * g * g * g / 24.0);
-    s = fma(s, f, g * g * g / 6.0);
-    s = fma(s, f, g * g / 2.0);
-    s = fma(s, f, g);
+};
+
+struct EighthSeries {
+  double c[6];
+  __device__ __forceinline__ EighthSeries() {
+    constexpr double g = 0.69314718055994530942 / 8.0;
+    c[0] = g, c[1] = g * g / 2.0, c[2] = g * g * g / 6.0, c[3] = g * g * g * g / 24.0;
+    c[4] = g * g * g * g * g / 120.0, c[5] = g * g * g * g * g * g / 720.0;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) asm("" : "+s"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double f) const {
+    double s = fma(c[5], f, c[4]);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) s = fma(s, f, c[i]);
     return fma(s, f, 1.0);
   }
 };
+
+// log(w / total) for 0 < w <= total, in fp64: the exponents' difference, and
+// the mantissas' ratio (brought within sqrt(2) of 1) by 2 atanh((a - b) / (a +
+// b)), whose series to the 17th power leaves less than 0.1716^19 / 19 = 2e-16.
+__device__ __forceinline__ double log_ratio(double w, double total) {
+  double a = __builtin_amdgcn_frexp_mant(w);
+  const double b = __builtin_amdgcn_frexp_mant(total);
+  int e = __builtin_amdgcn_frexp_exp(w) - __builtin_amdgcn_frexp_exp(total);
+  if (a > 1.4142135623730951 * b) a *= 0.5, ++e;
+  else if (1.4142135623730951 * a < b) a *= 2.0, --e;
+  const double s = (a - b) / (a + b);
+  const double z = s * s;
+  double t = 1.0 / 17.0;
+#pragma unroll
+  for (int i = 15; i > 0; i -= 2) t = fma(t, z, 1.0 / i);
+  return fma(static_cast<double>(e), 0.69314718055994530942, 2.0 * s * t);
+}
 
 // Geometry of the scan. A row is read in 16-byte pieces at 16-byte aligned
 // addresses: element e of the row's pieces is position e - lead, lead the
 // elements between the aligned address and the row's start.
 constexpr int kScanElems = 16;             // elements per thread of a scan workgroup
-constexpr int kScanBins = 512;             // mass histogram: bins of 1/16 bit below the chunk's maximum
+constexpr int kScanBins = 512;             // mass histogram: bins of 1/8 bit below the chunk's maximum
 constexpr int kCandidates = 4096;          // entries that k_sample_pick settles in LDS,
 constexpr int kWaveCandidates = 128;       // and how many of them by one wave
 constexpr int kFlatRow = 1024;             // kept entries above which only the border's are gathered
@@ -182,6 +210,7 @@ struct SampleParams {
   int64_t ld_ids;
   const float* u;
   fkl_sample_params set;
+  double c;  // log2(e) / T of the shared temperature
   int32_t* token;
   float* logprob;
   int32_t V;
@@ -217,7 +246,7 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& P, int64
   // the first entry alone: greedy, or a filter that only it can pass
   const bool first = T == 0.0f || p <= 0.0f || q > 1.0f;
   s.k = first ? 1u : (k <= 0 || k >= P.V) ? 0x7fffffffu : static_cast<uint32_t>(k);
-  s.c = T > 0.0f ? 1.4426950408889634074 / static_cast<double>(T) : 1.0;
+  s.c = !(T > 0.0f) ? 1.0 : P.set.temperature_rows ? 1.4426950408889634074 / static_cast<double>(T) : P.c;
   s.p = first || !(p < 1.0f) ? 1.0 : static_cast<double>(p);
   s.q = first || !(q > 0.0f) ? 0.0 : static_cast<double>(q);
   s.u = u > 0.0f ? static_cast<double>(fminf(u, 1.0f)) : 0.0;
@@ -317,10 +346,10 @@ __device__ __forceinline__ void put_none(const SampleParams& P, int64_t row) {
   if (P.logprob) dstore(P.dbg, 4, kDbgSampleOut, P.logprob + row, -INFINITY);
 }
 
-__device__ __forceinline__ void put_draw(const SampleParams& P, int64_t row, int at, double prob) {
+__device__ __forceinline__ void put_draw(const SampleParams& P, int64_t row, int at, double w, double total) {
   const int32_t id = P.ids ? dload(P.dbg, 1, kDbgSampleLogits, P.ids + row * P.ld_ids + at) : at;
   dstore(P.dbg, 3, kDbgSampleOut, P.token + row, id);
-  if (P.logprob) dstore(P.dbg, 4, kDbgSampleOut, P.logprob + row, static_cast<float>(log(prob)));
+  if (P.logprob) dstore(P.dbg, 4, kDbgSampleOut, P.logprob + row, static_cast<float>(log_ratio(w, total)));
 }
 
 constexpr int kDigits = 256;
@@ -439,7 +468,7 @@ __device__ __forceinline__ void sample_row_exact(const SampleParams& P, int64_t 
   for (int i = tid; i < V; i += kRowThreads) mine += kept(i);
   const double total = block_sum_f64(mine, shared);
   const int at = find_position(kept, V, S.u * total, shared);
-  if (tid == 0) put_draw(P, row, at, kept(at) / total);
+  if (tid == 0) put_draw(P, row, at, kept(at), total);
 }
 
 // ---------------------------------------------------------------------------
@@ -516,17 +545,19 @@ struct RowView {
   }
 };
 
-// The mass histogram's grid: entry x lies in bin rint(16 x log2(e) / T), a
-// monotone function of x, with the weight 2^(f / 16) relative to the bin's
+// The mass histogram's grid: entry x lies in bin rint(8 x log2(e) / T), a
+// monotone function of x, with the weight 2^(f / 8) relative to the bin's
 // centre. A histogram word holds the number of entries from bit 49 up, and
-// below it their weights in units of 2^-34 (16384 entries of at most 2^(1/32)
+// below it their weights in units of 2^-34 (16384 entries of at most 2^(1/16)
 // stay below 2^49). The rounding is 2^-35 of a weight either way: over n
 // entries the sums are off by sqrt(n) 2^-35 of a weight, and a draw differs
 // from that of exact sums with a probability below 1e-8 at 2^18 entries.
 // Integer sums do not depend on their order.
 constexpr int kHistShift = 34;
 constexpr int kHistCount = 49;
-constexpr double kMaxBin = 16777216.0;  // rows beyond it are left to sample_row_exact
+// Rows that the grid does not fit are left to sample_row_exact: bins beyond
+// 2^24, or so wide that the last one's lower end is beyond fp32.
+__device__ __forceinline__ bool grid_fits(double base, double c8) { return fabs(base) < 16777216.0 && c8 > 1e-30; }
 
 __device__ __forceinline__ uint32_t hist_count(uint64_t w) { return static_cast<uint32_t>(w >> kHistCount); }
 __device__ __forceinline__ uint64_t hist_units(uint64_t w) { return w & ((uint64_t(1) << kHistCount) - 1); }
@@ -536,14 +567,14 @@ __device__ __forceinline__ double units_mass(uint64_t units) {
 
 // One entry's histogram word: its weight is rounded to units by adding 1.5 *
 // 2^18, whose last place is 2^-34.
-__device__ __forceinline__ uint64_t hist_word(const Sixteenths& x) {
+__device__ __forceinline__ uint64_t hist_word(const EighthSeries& power, const Eighths& x) {
   constexpr uint64_t kBits = 0x4118000000000000ull;  // of 1.5 * 2^18
-  return static_cast<uint64_t>(__double_as_longlong(x.fraction() + 393216.0)) +
+  return static_cast<uint64_t>(__double_as_longlong(power(x.f) + 393216.0)) +
          ((uint64_t(1) << kHistCount) - kBits);
 }
 
 // One workgroup per chunk of a row. HBM bound where only the maxima are
-// wanted; with the masses, one fp64 exponential per entry (about 17 vector
+// wanted; with the masses, one fp64 exponential per entry (about 20 vector
 // instructions, and an LDS atomic for the histogram) takes longer than the
 // reading.
 template <class T, int kThreads>
@@ -552,7 +583,7 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   constexpr int kPieces = kScanElems / kPer;
   constexpr int kWaves = kThreads / 64;
   __shared__ uint64_t hist[kScanBins];
-  __shared__ double sixteenth[16];
+  __shared__ double eighth[8];
   __shared__ float wave_top[kWaves];
   __shared__ double wave_mass[kWaves];
   const int tid = threadIdx.x;
@@ -596,12 +627,13 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   if (lane == 0) wave_top[tid >> 6] = top;
   if (mode == kMassHistogram)
     for (int i = tid; i < kScanBins; i += kThreads) hist[i] = 0;
-  else if (tid < 16)
-    sixteenth[tid] = exp2_f64(tid * (1.0 / 16.0));
+  else if (tid < 8)
+    eighth[tid] = exp2_f64(tid * (1.0 / 8.0));
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) top = fmaxf(top, wave_top[w]);
-  const double c16 = 16.0 * S.c;
+  const double c8 = 8.0 * S.c;
+  const EighthSeries power;
   double sum = 0.0;
   if (mode == kChunkMass) {
     if (top == INFINITY) {
@@ -610,34 +642,35 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum += x[p][j] == INFINITY ? 1.0 : 0.0;
     } else if (top > -INFINITY) {
-      // 2^(t / 16) as the fraction's power, a sixteenth's and an exponent; what
+      // 2^(t / 8) as the fraction's power, an eighth's and an exponent; what
       // lies 2^-1000 below the chunk's largest (masked entries among it) adds
       // as much as nothing
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          const Sixteenths e(fmax((static_cast<double>(x[p][j]) - static_cast<double>(top)) * c16, -16000.0));
-          const double w = e.fraction() * sixteenth[e.b & 15];
-          sum += __hiloint2double(__double2hiint(w) + ((e.b >> 4) << 20), __double2loint(w));
+          const Eighths e(fmax((static_cast<double>(x[p][j]) - static_cast<double>(top)) * c8, -8000.0));
+          const double w = power(e.f) * eighth[e.b & 7];
+          sum += __hiloint2double(__double2hiint(w) + ((e.b >> 3) << 20), __double2loint(w));
         }
     }
   } else {
-    const double base = rint(static_cast<double>(top) * c16);
-    if (fabs(base) < kMaxBin) {
+    const double base = rint(static_cast<double>(top) * c8);
+    if (grid_fits(base, c8)) {
       const int first = static_cast<int>(base);
+      // What lies below the last bin, 2^-64 of the chunk's largest weight, is
+      // left out: of 2^18 entries all together less than 2^-46 of the mass.
+      // Masked entries and NaN are brought there.
+      const float low = static_cast<float>((base - 2.0 * kScanBins) / c8);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          // masked entries and what lies 2^-256 below the chunk's largest: all in one place, of no weight
-          const double t = fmax(static_cast<double>(x[p][j]) * c16, base - 4096.0);
-          const Sixteenths e(t);
+          const Eighths e(static_cast<double>(fmaxf(x[p][j], low)) * c8);
           const uint32_t d = static_cast<uint32_t>(first - e.b);
           if (d < kScanBins)
-            atomicAdd(reinterpret_cast<unsigned long long*>(&hist[d]), static_cast<unsigned long long>(hist_word(e)));
-          else  // 2^-32 of the chunk's largest weight or less: fp32's relative precision is enough
-            sum += static_cast<double>(exp2f(static_cast<float>((t - base) * (1.0 / 16.0))));
+            atomicAdd(reinterpret_cast<unsigned long long*>(&hist[d]),
+                      static_cast<unsigned long long>(hist_word(power, e)));
         }
     }
     __syncthreads();
@@ -682,8 +715,8 @@ struct PickLds {
       uint64_t units[kRowThreads];
     } fine;
   };
-  double bin_scale[kScanBins];  // 2^(-d / 16)
-  double sixteenth[16];         // 2^(j / 16)
+  double bin_scale[kScanBins];  // 2^(-d / 8)
+  double eighth[8];             // 2^(j / 8)
   double chunk[kMaxChunks];
   uint64_t chunk_units[kMaxChunks];
   int32_t chunk_off[kMaxChunks];
@@ -763,20 +796,17 @@ __device__ __forceinline__ void sort_wave(uint32_t (&s)[R]) {
 
 // Border and draw among 64 R entries held by one wave, entry l R + r in lane l
 // (keys at or below kMaskedKey: none). whole: the mass that top-p goes by, or
-// negative for that of the first k entries. Returns the entry drawn, prob its
-// probability, to every lane. At least one entry must be unmasked.
+// negative for that of the first k entries. Returns the entry drawn, with its
+// weight and that of all kept entries, to every lane. At least one entry must
+// be unmasked.
 template <int R>
 __device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSettings& S, float m, uint32_t m_key,
-                                           double whole, double& prob) {
+                                           double whole, double& w_at, double& kept) {
   const int lane = threadIdx.x & 63;
-  uint32_t edge = kMaskedKey + 1;
-  uint32_t quota = 0xffffffffu;  // of the entries equal to the edge, the first this many are kept
-  uint32_t ties = 0;
-  double w[R];
-  const bool ordered = S.k < 64 * R || S.p < 1.0;
-  if (ordered) {
+  double w[R];  // of the entries kept, in their own order
+  if (S.k < 64 * R || S.p < 1.0) {
     uint32_t s[R];
-    bool falls = true;  // already in order, as a teacher cache's lists are
+    bool falls = true;  // in order already, as a teacher cache's lists are
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] = key[r];
@@ -784,14 +814,15 @@ __device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSe
     }
     const uint32_t next = dpp<0x130>(key[0]);  // of the following lane; 0 at the end
     falls = falls && key[R - 1] >= next;
-    if (__ballot(falls) != ~uint64_t(0)) sort_wave<R>(s);
+    const bool ordered = __ballot(falls) == ~uint64_t(0);
+    if (!ordered) sort_wave<R>(s);
     double mine = 0.0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       w[r] = static_cast<uint32_t>(lane * R + r) < S.k ? weight_of(s[r], m, m_key, S.c) : 0.0;
       mine += w[r];
     }
-    const double incl = wave_scan(mine);
+    double incl = wave_scan(mine);
     const double target = S.p * (whole < 0.0 ? from_lane(incl, 63) : whole);
     double run = incl - mine;
     uint32_t n_kept = 0;
@@ -802,37 +833,49 @@ __device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSe
       n_kept += __popcll(__ballot(keep));
       run += w[r];
     }
-    const uint32_t last = n_kept > 0 ? n_kept - 1 : 0;
+    if (n_kept == 0) n_kept = 1;
+    if (ordered) {  // the kept entries are the first ones
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r == static_cast<int>(last % R)) edge = from_lane(s[r], static_cast<int>(last / R));
-    uint32_t above = 0;
+      for (int r = 0; r < R; ++r)
+        if (static_cast<uint32_t>(lane * R + r) >= n_kept) w[r] = 0.0;
+    } else {
+      const uint32_t last = n_kept - 1;
+      uint32_t edge = 0, above = 0, ties = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r == static_cast<int>(last % R)) edge = from_lane(s[r], static_cast<int>(last / R));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        above += __popcll(__ballot(s[r] > edge));
+        ties += __popcll(__ballot(s[r] == edge));
+      }
+      // of the entries equal to the edge, the first this many are kept
+      const uint32_t quota = n_kept - above;
+      uint32_t before = 0;
+      if (quota < ties) {
+        uint32_t equal = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) equal += key[r] == edge;
+        before = wave_scan(equal) - equal;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool in = key[r] > edge || (key[r] == edge && (quota >= ties || before++ < quota));
+        w[r] = in ? weight_of(key[r], m, m_key, S.c) : 0.0;
+      }
+    }
+  } else {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      above += __popcll(__ballot(s[r] > edge));
-      ties += __popcll(__ballot(s[r] == edge));
+      w[r] = weight_of(key[r], m, m_key, S.c);
+      if (w[r] < S.q) w[r] = 0.0;
     }
-    quota = last + 1 - above;
-  }
-  uint32_t before = 0;
-  if (quota < ties) {  // the border falls inside a group of equal entries
-    uint32_t mine = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) mine += key[r] == edge;
-    before = wave_scan(mine) - mine;
-  } else {
-    quota = 0xffffffffu;
   }
   double mine = 0.0;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const bool in = key[r] > edge || (key[r] == edge && before++ < quota);
-    w[r] = in ? weight_of(key[r], m, m_key, S.c) : 0.0;
-    if (!ordered && w[r] < S.q) w[r] = 0.0;
-    mine += w[r];
-  }
+  for (int r = 0; r < R; ++r) mine += w[r];
   const double incl = wave_scan(mine);
-  const double kept = from_lane(incl, 63);
+  kept = from_lane(incl, 63);
   const double goal = S.u * kept;
   double run = incl - mine;
   int hit = R, last = 0;
@@ -848,7 +891,7 @@ __device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSe
   const uint64_t hits = __ballot(hit < R);
   const uint64_t any = __ballot(w_last > 0.0);
   const int l = hits ? __ffsll(static_cast<long long>(hits)) - 1 : 63 - __clzll(static_cast<long long>(any));
-  prob = (hits ? from_lane(w_hit, l) : from_lane(w_last, l)) / kept;
+  w_at = hits ? from_lane(w_hit, l) : from_lane(w_last, l);
   return l * R + static_cast<int>(from_lane(static_cast<uint32_t>(hits ? hit : last), l));
 }
 
@@ -874,9 +917,9 @@ __global__ __launch_bounds__(256) void k_sample_short(SampleParams P, int64_t ro
     if (lane == 0) put_none(P, row);
     return;
   }
-  double prob;
-  const int at = settle_wave<R>(key, S, key_logit(m_key), m_key, -1.0, prob);
-  if (lane == 0) put_draw(P, row, at, prob);
+  double w, total;
+  const int at = settle_wave<R>(key, S, key_logit(m_key), m_key, -1.0, w, total);
+  if (lane == 0) put_draw(P, row, at, w, total);
 }
 
 // Distance of a key from the largest, in bins for bound_of_kth: exact below
@@ -922,13 +965,13 @@ __device__ __forceinline__ uint32_t bound_of_kth(PickLds& L, int groups, uint32_
 
 // The lowest key in (kMaskedKey, m_key] whose bin is at least b; m_key + 1 if
 // there is none. Each step tests 64 keys of the range, one per lane.
-__device__ __forceinline__ uint32_t first_key_of_bin(double b, double c16, uint32_t m_key) {
+__device__ __forceinline__ uint32_t first_key_of_bin(double b, double c8, uint32_t m_key) {
   const uint32_t lane = threadIdx.x & 63;
   uint64_t lo = kMaskedKey + 1, hi = static_cast<uint64_t>(m_key) + 1;
   while (lo < hi) {
     const uint64_t step = (hi - lo) / 64 + 1;
     const uint64_t at = lo + lane * step;
-    const bool in = at >= hi || rint(static_cast<double>(key_logit(static_cast<uint32_t>(at))) * c16) >= b;
+    const bool in = at >= hi || rint(static_cast<double>(key_logit(static_cast<uint32_t>(at))) * c8) >= b;
     const uint64_t hit = __ballot(in);
     const int f = hit ? __ffsll(static_cast<long long>(hit)) - 1 : 64;
     if (f < 64) hi = min(hi, lo + f * step);
@@ -938,12 +981,12 @@ __device__ __forceinline__ uint32_t first_key_of_bin(double b, double c16, uint3
   return static_cast<uint32_t>(lo);
 }
 
-// 2^(t / 16) for t <= 16, by the table L.sixteenth; 0 below 2^-1000.
+// 2^(t / 8) for t <= 8, by the table L.eighth; 0 below 2^-1000.
 __device__ __forceinline__ double power(const PickLds& L, double t) {
-  const Sixteenths e(fmax(t, -16000.0));
-  const double w = e.fraction() * L.sixteenth[e.b & 15];
-  const double v = __hiloint2double(__double2hiint(w) + ((e.b >> 4) << 20), __double2loint(w));
-  return t < -16000.0 ? 0.0 : v;
+  const Eighths e(fmax(t, -8000.0));
+  const double w = EighthSeries()(e.f) * L.eighth[e.b & 7];
+  const double v = __hiloint2double(__double2hiint(w) + ((e.b >> 3) << 20), __double2loint(w));
+  return t < -8000.0 ? 0.0 : v;
 }
 
 // The draw within one chunk, from the first position at which base plus the
@@ -988,7 +1031,7 @@ __device__ __forceinline__ void draw_in_chunk(const SampleParams& P, int64_t row
   // if rounding leaves no such position, the last one kept
   const bool found = L.word[0] != 0xffffffffu;
   const int at = static_cast<int>(found ? L.word[0] : L.word[1]);
-  if (found ? first_at == at : last_at == at) put_draw(P, row, at, (found ? first_w : last_w) / kept);
+  if (found ? first_at == at : last_at == at) put_draw(P, row, at, found ? first_w : last_w, kept);
 }
 
 // The chunk in which the running sum of L.chunk[0 .. n), n <= 64, exceeds the
@@ -1010,8 +1053,8 @@ __device__ __forceinline__ int find_chunk(const PickLds& L, int n, double u, dou
 
 // What the mass histograms say of a row.
 struct RowHistogram {
-  double c16, base;   // the grid, and the bin of the row's largest logit
-  double whole;       // the row's mass relative to 2^(base / 16)
+  double c8, base;   // the grid, and the bin of the row's largest logit
+  double whole;       // the row's mass relative to 2^(base / 8)
   uint32_t border;    // the bin (from the top) in which the mass reaches target, or the count top-k
   uint32_t in_border, above;  // entries in it and above it
   double mass_above;
@@ -1023,17 +1066,14 @@ struct RowHistogram {
 __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slot, const RowSettings& S, float m,
                                               PickLds& L, RowHistogram& H) {
   const int tid = threadIdx.x;
-  H.c16 = 16.0 * S.c;
-  H.base = rint(static_cast<double>(m) * H.c16);
-  if (!(fabs(H.base) < kMaxBin)) return false;
-  double rest = 0.0;
+  H.c8 = 8.0 * S.c;
+  H.base = rint(static_cast<double>(m) * H.c8);
+  if (!grid_fits(H.base, H.c8)) return false;
   if (tid < P.chunks) {
     const uint32_t ck = dload(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot + tid);
-    const double cm = dload(P.dbg, 5, kDbgSampleWork, P.chunk_mass + slot + tid);
     // chunk bin i is row bin i + off; a masked chunk's are all empty
-    const double off = ck > kMaskedKey ? H.base - rint(static_cast<double>(key_logit(ck)) * H.c16) : 1e6;
+    const double off = ck > kMaskedKey ? H.base - rint(static_cast<double>(key_logit(ck)) * H.c8) : 1e6;
     L.chunk_off[tid] = static_cast<int>(fmin(off, 1e6));
-    rest = cm * power(L, -off);
   }
   if (tid < kScanBins) L.bin_scale[tid] = power(L, -tid);
   if (tid == 0) L.word[2] = 0xffffffffu;
@@ -1045,25 +1085,17 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
   constexpr int kBatch = 8;  // words read before any is used
   for (int c0 = tid / kScanBins; c0 < P.chunks; c0 += kBatch * (kRowThreads / kScanBins)) {
     uint64_t w[kBatch];
-    int off[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int ch = c0 + b * (kRowThreads / kScanBins);
       w[b] = 0;
       if (ch < P.chunks) {
-        off[b] = L.chunk_off[ch];
-        // row bin `bin` where the chunk has it, otherwise the chunk bin that lies below the row's last
-        const int i = off[b] >= kScanBins ? bin : (bin - off[b]) & (kScanBins - 1);
-        w[b] = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + i);
+        const int off = L.chunk_off[ch];
+        if (off <= bin) w[b] = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + bin - off);
       }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (w[b] == 0) continue;
-      const double v = units_mass(hist_units(w[b]));
-      if (off[b] <= bin) count += hist_count(w[b]), mass += v;
-      else rest += v * power(L, -(off[b] >= kScanBins ? off[b] + bin : bin + kScanBins));
-    }
+    for (int b = 0; b < kBatch; ++b) count += hist_count(w[b]), mass += units_mass(hist_units(w[b]));
   }
   if constexpr (kRowThreads > kScanBins) {
     if (tid >= kScanBins) L.half.count[bin] = count, L.half.mass[bin] = mass;
@@ -1072,12 +1104,9 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
     else count = 0, mass = 0.0;
   }
   const double scaled = tid < kScanBins ? mass * L.bin_scale[bin] : 0.0;
-  double in_bins, rest_all;
   uint32_t counted;
-  const double above = block_scan(scaled, L.wave_f64[0], in_bins);
-  block_scan(rest, L.wave_f64[1], rest_all);
+  const double above = block_scan(scaled, L.wave_f64[0], H.whole);
   const uint32_t count_above = block_scan(count, L.wave_u32[2], counted);
-  H.whole = in_bins + rest_all;
   H.target = S.p * H.whole;
   const bool here = S.k < static_cast<uint32_t>(P.V) ? count_above < S.k && count_above + count >= S.k
                                                      : above < H.target && above + scaled >= H.target;
@@ -1216,7 +1245,8 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
 
 // A row of which more entries are kept than the workgroup holds: the bins
 // above the border are kept whole, and only the border bin's entries are
-// gathered (one read of the row) and settled. false where they are too many.
+// gathered (one read of the row, two where they are more than 4096) and
+// settled. false where thousands of them are equal.
 template <class T>
 __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row, const RowSettings& S,
                                               const RowView<T>& view, uint32_t m_key, PickLds& L,
@@ -1227,21 +1257,69 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
   const int V = P.V;
   const int64_t slot = row * P.chunks;
   const bool by_count = S.k < static_cast<uint32_t>(V);
-  if (H.in_border > kCandidates || (by_count && (S.p < 1.0 || S.q > 0.0))) return false;
-  const int n = static_cast<int>(H.in_border);
+  if (by_count && (S.p < 1.0 || S.q > 0.0)) return false;
   const double edge_bin = H.base - H.border;
   if (wave < 2) {
-    const uint32_t key = first_key_of_bin(edge_bin + wave, H.c16, m_key);
+    const uint32_t key = first_key_of_bin(edge_bin + wave, H.c8, m_key);
     if (lane == 0) L.word[wave] = key;
   }
   if (tid < P.chunks) L.chunk_units[tid] = 0;
   if (tid == 0) L.word[2] = 0;
   __syncthreads();
-  const uint32_t k_lo = L.word[0], k_hi = L.word[1];
-  const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
+  const uint32_t bin_end = L.word[1];
+  uint32_t k_lo = L.word[0], k_hi = bin_end;  // the keys among which the border lies
+  auto units = [&](uint32_t key) {
+    return hist_units(hist_word(EighthSeries(), Eighths(static_cast<double>(key_logit(key)) * H.c8)));
+  };
+  const double scale = L.bin_scale[H.border] * (1.0 / (uint64_t(1) << kHistShift));  // of the border bin's units
+  const double want = ceil((H.target - H.mass_above) / scale);
+  uint64_t target = by_count ? S.k - H.above : want < 1.0 ? 1 : static_cast<uint64_t>(want);
   constexpr int kPer = RowView<T>::kPer;
   const int pieces = (view.lead + V + kPer - 1) / kPer;
   constexpr int kBatch = 4;  // pieces read before any is looked at
+  int n = static_cast<int>(H.in_border);
+  if (n > kCandidates) {
+    // one more read of the row: the bin's entries counted into finer bins
+    const int shift = max(0, 32 - kFineBits - __clz(static_cast<int>((k_hi - k_lo - 1) | 1)));
+    const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
+    L.fine.count[tid] = 0;
+    L.fine.units[tid] = 0;
+    if (tid == 0) L.word[5] = 0;
+    __syncthreads();
+    for (int p0 = 0; p0 < pieces; p0 += kBatch * kRowThreads) {
+      u32x4 held[kBatch];
+      view.template batch<kBatch>(P.dbg, p0, kRowThreads, held);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const float x = view.logit(held[b], j);
+          if (x >= x_lo && x < x_hi) {
+            const uint32_t key = logit_key(x);
+            atomicAdd(&L.fine.count[(key - k_lo) >> shift], 1u);
+            atomicAdd(reinterpret_cast<unsigned long long*>(&L.fine.units[(key - k_lo) >> shift]),
+                      static_cast<unsigned long long>(units(key)));
+          }
+        }
+    }
+    __syncthreads();
+    const uint32_t here = L.fine.count[kRowThreads - 1 - tid];
+    uint64_t sum;
+    const uint64_t before =
+        block_scan(by_count ? uint64_t(here) : L.fine.units[kRowThreads - 1 - tid], L.wave_u64, sum);
+    put_last(&L.word[5], here > 0 && before < target, static_cast<uint32_t>(tid));
+    __syncthreads();
+    const int at = static_cast<int>(L.word[5]);
+    if (tid == at) L.word[6] = here, L.units = before;
+    __syncthreads();
+    n = static_cast<int>(L.word[6]);
+    target -= L.units;
+    k_lo += static_cast<uint32_t>(kRowThreads - 1 - at) << shift;
+    k_hi = static_cast<uint32_t>(min(static_cast<uint64_t>(k_hi), static_cast<uint64_t>(k_lo) + (uint64_t(1) << shift)));
+    if (n > kCandidates) return false;  // thousands of equal entries
+    __syncthreads();
+  }
+  const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi), x_end = key_logit(bin_end);
   uint32_t* const found = L.list;  // positions
   for (int p0 = 0; p0 < pieces; p0 += kBatch * kRowThreads) {  // the same for all lanes: they vote below
     const int i0 = p0 + tid;
@@ -1254,6 +1332,21 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
       for (int j = 0; j < kPer; ++j) {
         const float x = view.logit(held[b], j);
         hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << j;
+      }
+      if (x_hi < x_end) {  // the bin's entries above the finer one are kept: their chunk's mass
+        uint64_t kept = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const float x = view.logit(held[b], j);
+          if (x >= x_hi && x < x_end) kept += units(logit_key(x));
+        }
+        if (__ballot(kept != 0) != 0) {  // a wave's pieces lie in one chunk
+          const uint64_t all = from_lane(wave_scan(kept), 63);
+          if (lane == 0)
+            atomicAdd(reinterpret_cast<unsigned long long*>(
+                          &L.chunk_units[(i0 + b * kRowThreads) * kPer / P.chunk_elems]),
+                      static_cast<unsigned long long>(all));
+        }
       }
       if (__ballot(hits != 0) == 0) continue;
       const uint32_t mine = static_cast<uint32_t>(__popc(hits));
@@ -1272,12 +1365,6 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
     const uint32_t key = view.element(P.dbg, static_cast<int>(pos) + view.lead);
     L.entry[i] = (static_cast<uint64_t>(key) << 32) | ~pos;
   }
-  auto units = [&](uint32_t key) {
-    return hist_units(hist_word(Sixteenths(static_cast<double>(key_logit(key)) * H.c16)));
-  };
-  const double scale = L.bin_scale[H.border] * (1.0 / (uint64_t(1) << kHistShift));  // of the border bin's units
-  const double want = ceil((H.target - H.mass_above) / scale);
-  const uint64_t target = by_count ? S.k - H.above : want < 1.0 ? 1 : static_cast<uint64_t>(want);
   const uint64_t edge = border_entry(L, V, n, k_lo, k_hi, !by_count, target, [&](int i) { return L.entry[i]; }, units);
   const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
   const int edge_pos = static_cast<int>(~static_cast<uint32_t>(edge));
@@ -1308,7 +1395,7 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
   const int chunk = find_chunk(L, P.chunks, S.u, kept, goal, before);
   const float edge_x = key_logit(edge_key);
   draw_in_chunk(P, row, view, L, chunk, before, goal, kept, [&](float x, int pos) {
-    return x > edge_x || (x == edge_x && pos <= edge_pos) ? power(L, static_cast<double>(x) * H.c16 - H.base) : 0.0;
+    return x > edge_x || (x == edge_x && pos <= edge_pos) ? power(L, static_cast<double>(x) * H.c8 - H.base) : 0.0;
   });
   return true;
 }
@@ -1320,9 +1407,9 @@ __device__ __forceinline__ void settle_candidates(const SampleParams& P, int64_t
   uint32_t key[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) key[r] = lane * R + r < n ? L.cand.key[lane * R + r] : 0u;
-  double prob;
-  const int at = settle_wave<R>(key, S, m, m_key, whole, prob);
-  if (lane == 0) put_draw(P, row, L.cand.pos[at], prob);
+  double w, total;
+  const int at = settle_wave<R>(key, S, m, m_key, whole, w, total);
+  if (lane == 0) put_draw(P, row, L.cand.pos[at], w, total);
 }
 
 // Settles a row from what the scan left; false where the border is too wide
@@ -1352,7 +1439,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     if (S.p >= 1.0) {  // no filter: a chunk, then a position in it
       draw_in_chunk(P, row, view, L, chunk, base, goal, whole, [&](float x, int) {
         const double d = x == m ? 0.0 : static_cast<double>(x) - static_cast<double>(m);  // m may be infinite
-        return x > -INFINITY ? power(L, d * (16.0 * S.c)) : 0.0;
+        return x > -INFINITY ? power(L, d * (8.0 * S.c)) : 0.0;
       });
       return true;
     }
@@ -1373,8 +1460,8 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
     if (!row_histogram(P, slot, S, m, L, H)) return false;
     const bool wide = H.above + H.in_border > (all ? kFlatRow : kCandidates);
     if (wide && (all || S.p < 1.0 || S.q <= 0.0)) return pick_flat_row(P, row, S, view, m_key, L, H);
-    if (all) whole = H.whole * exp2_f64((H.base - static_cast<double>(m) * H.c16) * (1.0 / 16.0));
-    bound = max(bound, first_key_of_bin(H.base - H.border, H.c16, m_key));
+    if (all) whole = H.whole * exp2_f64((H.base - static_cast<double>(m) * H.c8) * (1.0 / 8.0));
+    bound = max(bound, first_key_of_bin(H.base - H.border, H.c8, m_key));
   }
 
   // The groups that reach the bound, in order, and their entries that do: the
@@ -1457,7 +1544,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   }
   auto weight = [&](uint32_t key) {
     const float x = key_logit(key);
-    return x == m ? 1.0 : power(L, (static_cast<double>(x) - static_cast<double>(m)) * (16.0 * S.c));
+    return x == m ? 1.0 : power(L, (static_cast<double>(x) - static_cast<double>(m)) * (8.0 * S.c));
   };
   constexpr double kUnit = static_cast<double>(uint64_t(1) << 46);  // 4096 weights of at most 1 stay below 2^59
   auto units = [&](uint32_t key) { return static_cast<uint64_t>(weight(key) * kUnit + 0.5); };
@@ -1509,7 +1596,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   __syncthreads();
   if (tid == 0) {
     const uint32_t i = L.word[2] != 0xffffffffu ? L.word[2] : L.word[3];
-    put_draw(P, row, L.cand.pos[i], weight(L.cand.key[i]) / total);
+    put_draw(P, row, L.cand.pos[i], weight(L.cand.key[i]), total);
   }
   return true;
 }
@@ -1535,7 +1622,7 @@ __global__ __launch_bounds__(kRowThreads) void k_sample_pick(SampleParams P, int
   const RowView<T> view(P, row);
   m_key = wave_max_u32(m_key);
   if ((tid & 63) == 0) L.wave_u32[0][tid >> 6] = m_key;
-  if (tid < 16) L.sixteenth[tid] = exp2_f64(tid * (1.0 / 16.0));
+  if (tid < 8) L.eighth[tid] = exp2_f64(tid * (1.0 / 8.0));
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kRowWaves; ++w) m_key = max(m_key, L.wave_u32[0][w]);
@@ -1614,6 +1701,7 @@ hipError_t launch_sample(const SamplePlan& p, const SampleArgs& a, hipStream_t s
   P.logits = a.logits, P.ld = p.ld;
   P.ids = a.ids, P.ld_ids = p.ld_ids;
   P.u = a.u, P.set = a.params;
+  P.c = 1.4426950408889634074 / static_cast<double>(a.params.temperature);  // not used where T = 0
   P.token = a.token, P.logprob = a.logprob;
   P.V = static_cast<int32_t>(p.V);
   P.groups = static_cast<int32_t>(p.groups);

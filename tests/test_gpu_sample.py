@@ -156,6 +156,11 @@ def test_sample_extreme_temperatures_and_settings(V):
               dict(q=2.0), dict(q=-3.0), dict(k=-5), dict(k=2 ** 31 - 1), dict(T=1e-3, q=1e-30, p=0.999999)):
         print(f"[sample] extremes V={V} {s}", flush=True)
         _check(x, u, **s)
+    x[:, ::2] = float("-inf")
+    for s in (dict(T=1e30, p=0.5), dict(T=3e38, p=0.9), dict(T=3e38), dict(T=1e-30, p=0.5), dict(T=1e37, k=V // 4)):
+        print(f"[sample] extremes V={V} {s}, half masked", flush=True)
+        _check(x, u, **s)
+    x = torch.nan_to_num(x, neginf=-3.0)
     bad = torch.tensor([-1.0, float("nan"), float("inf"), 1.0, 0.0, float("-inf")], device=dev)
     token, logprob = _check(x, u, T=bad)
     assert token[[0, 1, 2, 5]].tolist() == [-1] * 4 and (token[[3, 4]] >= 0).all()
@@ -194,7 +199,7 @@ def test_sample_the_longest_rows(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("N,V", [(3, 60000), (40, 30000), (600, 20000)])
+@pytest.mark.parametrize("N,V", [(3, 60000), (40, 30000), (600, 20000), (3, 262000)])
 def test_sample_flat_rows(N, V, dtype):
     """Rows in which top-p keeps tens of thousands of entries, and rows whose
     entries nearly all weigh the same."""
