@@ -200,7 +200,8 @@ constexpr int kScanElems = 16;             // elements per thread of a scan work
 constexpr int kScanBins = 512;             // mass histogram: bins of 1/8 bit below the chunk's maximum
 constexpr int kCandidates = 4096;          // entries that k_sample_pick settles in LDS,
 constexpr int kWaveCandidates = 128;       // and how many of them by one wave
-constexpr int kFlatRow = 1024;             // kept entries above which only the border's are gathered
+constexpr int kFlatRow = 1024;             // kept entries above which only the border's are gathered,
+constexpr int kFlatEntries = 6144;         // at most this many of them
 constexpr int kShortRow = 1024;
 
 struct SampleParams {
@@ -413,13 +414,32 @@ __device__ __forceinline__ void sample_row_exact(const SampleParams& P, int64_t 
     for (int shift_bits = 24; shift_bits >= 0; shift_bits -= 8) {
       if (tid < kDigits) count[tid] = 0, mass[tid] = 0;
       __syncthreads();
-      for (int i = tid; i < V; i += kRowThreads) {
-        const uint32_t key = key_at(i);
-        if (shift_bits < 24 && (key >> (shift_bits + 8)) != prefix) continue;
-        if (!inside(key, i)) continue;
+      for (int i0 = 0; i0 < V; i0 += kRowThreads) {  // the same for all lanes: they vote
+        const int i = i0 + tid;
+        const uint32_t key = i < V ? key_at(i) : 0u;
+        bool left = i < V && (shift_bits == 24 || (key >> (shift_bits + 8)) == prefix) && inside(key, i);
         const uint32_t d = (key >> shift_bits) & 255u;
-        atomicAdd(&count[d], 1u);
-        if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&mass[d]), static_cast<unsigned long long>(fixed(key)));
+        const uint64_t units = left && by_mass ? fixed(key) : 0;
+        // the first digits are shared by most of a wave's entries, and atomics
+        // of many lanes on one address are carried out one after the other: the
+        // first few digits met are added up across the wave
+        for (int t = 0; t < 3; ++t) {
+          const uint64_t todo = __ballot(left);
+          if (todo == 0) break;
+          const int lead = __ffsll(static_cast<long long>(todo)) - 1;
+          const bool mine = left && d == from_lane(d, lead);
+          const uint64_t same = __ballot(mine);
+          const uint64_t sum = by_mass ? from_lane(wave_scan(mine ? units : uint64_t(0)), 63) : 0;
+          if ((tid & 63) == lead) {
+            atomicAdd(&count[d], static_cast<uint32_t>(__popcll(same)));
+            if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&mass[d]), static_cast<unsigned long long>(sum));
+          }
+          left = left && !mine;
+        }
+        if (left) {
+          atomicAdd(&count[d], 1u);
+          if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(&mass[d]), static_cast<unsigned long long>(units));
+        }
       }
       __syncthreads();
       if (tid == 0) {
@@ -695,17 +715,21 @@ static_assert(1 << kFineBits == kRowThreads, "one of border_entry's bins per thr
 constexpr int kMaxChunks = 64;
 
 struct PickLds {
-  uint32_t group_max[kMaxGroups];
   union {
     struct {
-      uint32_t key[kCandidates];
-      int32_t pos[kCandidates];
-    } cand;
-    uint64_t entry[kCandidates];  // (key, ~position) of the border bin's entries
-    struct {
-      uint32_t count[kScanBins];
-      double mass[kScanBins];
-    } half;  // the second half of the block's sums over the chunks
+      uint32_t group_max[kMaxGroups];
+      union {
+        struct {
+          uint32_t key[kCandidates];
+          int32_t pos[kCandidates];
+        } cand;
+        struct {
+          uint32_t count[kScanBins];
+          double mass[kScanBins];
+        } half;  // the second half of the block's sums over the chunks
+      };
+    };
+    uint64_t entry[kFlatEntries];  // (key, ~position) of a flat row's border bin
   };
   union {
     uint32_t bins[kDistanceBins];
@@ -1245,7 +1269,7 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
 
 // A row of which more entries are kept than the workgroup holds: the bins
 // above the border are kept whole, and only the border bin's entries are
-// gathered (one read of the row, two where they are more than 4096) and
+// gathered (one read of the row, two where they are more than 6144) and
 // settled. false where thousands of them are equal.
 template <class T>
 __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row, const RowSettings& S,
@@ -1278,7 +1302,7 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
   const int pieces = (view.lead + V + kPer - 1) / kPer;
   constexpr int kBatch = 4;  // pieces read before any is looked at
   int n = static_cast<int>(H.in_border);
-  if (n > kCandidates) {
+  if (n > kFlatEntries) {
     // one more read of the row: the bin's entries counted into finer bins
     const int shift = max(0, 32 - kFineBits - __clz(static_cast<int>((k_hi - k_lo - 1) | 1)));
     const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi);
@@ -1316,11 +1340,10 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
     target -= L.units;
     k_lo += static_cast<uint32_t>(kRowThreads - 1 - at) << shift;
     k_hi = static_cast<uint32_t>(min(static_cast<uint64_t>(k_hi), static_cast<uint64_t>(k_lo) + (uint64_t(1) << shift)));
-    if (n > kCandidates) return false;  // thousands of equal entries
+    if (n > kFlatEntries) return false;  // thousands of equal entries
     __syncthreads();
   }
   const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi), x_end = key_logit(bin_end);
-  uint32_t* const found = L.list;  // positions
   for (int p0 = 0; p0 < pieces; p0 += kBatch * kRowThreads) {  // the same for all lanes: they vote below
     const int i0 = p0 + tid;
     u32x4 held[kBatch];
@@ -1355,15 +1378,14 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
       if (lane == 63) at = atomicAdd(&L.word[2], incl);
       at = from_lane(at, 63) + incl - mine;
       const int pos = (i0 + b * kRowThreads) * kPer - view.lead;
-      for (; hits; hits &= hits - 1, ++at)
-        if (at < kCandidates) found[at] = static_cast<uint32_t>(pos + __ffs(static_cast<int>(hits)) - 1);
+      for (; hits; hits &= hits - 1, ++at) {
+        const int j = __ffs(static_cast<int>(hits)) - 1;
+        float x = view.logit(held[b], 0);
+#pragma unroll
+        for (int i = 1; i < kPer; ++i) x = i == j ? view.logit(held[b], i) : x;
+        if (at < kFlatEntries) L.entry[at] = (static_cast<uint64_t>(logit_key(x)) << 32) | ~static_cast<uint32_t>(pos + j);
+      }
     }
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kRowThreads) {
-    const uint32_t pos = found[i];
-    const uint32_t key = view.element(P.dbg, static_cast<int>(pos) + view.lead);
-    L.entry[i] = (static_cast<uint64_t>(key) << 32) | ~pos;
   }
   const uint64_t edge = border_entry(L, V, n, k_lo, k_hi, !by_count, target, [&](int i) { return L.entry[i]; }, units);
   const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
