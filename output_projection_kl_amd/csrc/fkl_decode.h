@@ -33,6 +33,7 @@ constexpr int kDecodeDebugBits = 6;
 enum ProjectShapeId {
   kProjectSkinny,
   kProject16x64,
+  kProject32x64,
   kProject64,
   kProject64x128,
   kProject128,
@@ -41,9 +42,17 @@ enum ProjectShapeId {
   kProject256
 };
 
+// How the block tiles read B. Once: with the hint that nothing else will ask
+// for it; by lines: each row in whole cache lines although it does not start
+// at one (for tiles of up to kProjectLinesRows rows).
+enum ProjectRead { kReadPlain, kReadOnce, kReadOnceByLines };
+constexpr int kProjectLinesRows = 32;
+
 struct ProjectPlan {
   int64_t M, N, K, lda, ldb, ldo;
   int a_type, out_type;
+  int64_t row_a;            // bytes of a quantised row of a in the workspace
+  bool once;                // every byte of b is read once, and b is larger than the last-level cache
   bool a_copied, b_copied;  // the 8-bit operand is copied to rows of round_up(K, 16) bytes
   ProjectShapeId shape;
   int splits;       // of the contraction, each of k_split bytes (1: none)

@@ -79,17 +79,29 @@ fkl_status debug_end(char* ws, hipStream_t stream) {
 
 namespace fkl {
 
+// A b larger than the last-level cache is not there at the next call. For up
+// to 256 rows it is read once, memory decides, and its loads say so (they are
+// non-temporal): 128256 x 4096 rows, 85 instead of 99 us for 8 rows of a, 91
+// instead of 105 for 30, 111 instead of 120 for 64, 149 instead of 155 for 200.
+// A b that the cache could hold is better kept there: 32000 x 4096, the same at
+// every call, took 30 us with the hint and 23 without. Rows that do not start
+// at cache lines share lines, which the hint lets go in between: such rows are
+// read by whole lines (up to 32 rows of a: 201088 x 2880, 101 instead of 115 us
+// for 16, 111 instead of 122 for 32), or without the hint (48: 129 us, 134 by
+// whole lines, 144 with the hint alone).
+constexpr int64_t kLastLevelBytes = int64_t(256) << 20;
+
 // The layout with the least estimated time, us. A block tile's stage (128
 // bytes of the contraction) takes `filled` of a CU that as many workgroups
 // share as fit, and `alone` for a workgroup with a CU to itself, whichever is
 // longer over the rounds that the tiles take; then the tile is stored. The
-// constants are fitted to the times of every layout at 157 sizes (M 1 to 8192,
+// constants are fitted to the times of the layouts at 157 sizes (M 1 to 8192,
 // N 64 to 201088, K 64 to 8192): the layout that they pick took 1.5% longer
 // than the fastest one in the mean. Both sides at some of them: 8192 x 8192 x
 // 4096 (M, N, K): 232 us as 256 x 256, 292 as 128 x 256, 328 as 128 x 128; 2048
-// x 4096 x 4096: 51, 39 and 44; 201 x 32003 x 2887: 50, 36 and 41; 48 x 128256 x
-// 4096: 121 as 64 x 128, 118 as 64 x 64, 153 as 16 x 64; 1 x 201088 x 2880: 110,
-// 106 and 100; 5 x 1024 x 1024: 6.1 as 16 x 16, 7.3 as 16 x 64; 1 x 128 x 5120:
+// x 4096 x 4096: 51, 39 and 44; 201 x 32003 x 2887: 50, 36 and 41; 48 x 32000 x
+// 4096: 37 as 64 x 128, 36 as 64 x 64; 32 x 32000 x 4096: 34 as 32 x 64, 37 as
+// 16 x 64; 5 x 1024 x 1024: 6.1 as 16 x 16, 7.3 as 16 x 64; 1 x 128 x 5120:
 // 8.7 as 16 x 16, 19.7 as 64 x 64, 10.8 of those with the contraction split.
 static void choose_project_shape(ProjectPlan* p) {
   struct Tile {
@@ -98,18 +110,24 @@ static void choose_project_shape(ProjectPlan* p) {
     double alone, filled;
   };
   static const Tile kTiles[] = {
-      {kProject16x64, 16, 64, 3, 0.21, 0.16},   {kProject64, 64, 64, 3, 0.28, 0.26},
-      {kProject64x128, 64, 128, 2, 0.80, 0.50}, {kProject128, 128, 128, 2, 0.85, 0.68},
-      {kProject128x256, 128, 256, 1, 0.75, 1.20}, {kProject256x128, 256, 128, 1, 0.76, 1.10},
-      {kProject256, 256, 256, 1, 1.07, 1.80},
+      {kProject16x64, 16, 64, 3, 0.21, 0.16},   {kProject32x64, 32, 64, 3, 0.24, 0.19},
+      {kProject64, 64, 64, 3, 0.28, 0.26},      {kProject64x128, 64, 128, 2, 0.80, 0.50},
+      {kProject128, 128, 128, 2, 0.85, 0.68},   {kProject128x256, 128, 256, 1, 0.75, 1.20},
+      {kProject256x128, 256, 128, 1, 0.76, 1.10}, {kProject256, 256, 256, 1, 1.07, 1.80},
   };
+  p->splits = 1;
+  p->k_split = p->K;
+  p->once = p->M <= 256 && p->N * (p->b_copied ? round_up(p->K, 16) : p->ldb) > kLastLevelBytes;
+  if (p->once) {
+    p->shape = p->M <= 16 ? kProject16x64 : p->M <= 32 ? kProject32x64 : p->M <= 64 ? kProject64x128
+             : p->M <= 128 ? kProject128x256 : kProject256;
+    return;
+  }
   const double kLaunch = 2.4;  // a launch's own time
   const double kJoin = 4.2;    // the second launch of a split contraction
   const double m = static_cast<double>(p->M), n = static_cast<double>(p->N), k = static_cast<double>(p->K);
   const double memory = (n * k + m * k + m * n * type_bytes(p->out_type)) / 6.5e6;
   const int64_t stages = ceil_div(p->K, 128);
-  p->splits = 1;
-  p->k_split = p->K;
   // 16 x 16 tiles, two workgroups a CU: one tile's latency, then less for each
   // further one; B is read again for every 16 rows
   const int64_t small = ceil_div(p->M, 16) * ceil_div(p->N, 16);
@@ -169,7 +187,9 @@ fkl_status make_project_plan(const fkl_project_shape* s, ProjectPlan* p) {
   const size_t row = static_cast<size_t>(round_up(s->K, 16));
   size_t off = kControlBytes;
   p->off_a = off;
-  if (p->a_copied || s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * row);
+  // a quantised a in rows that start at cache lines
+  p->row_a = round_up(s->K, s->a_type != FKL_I8 ? 128 : 16);
+  if (p->a_copied || s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M * p->row_a));
   p->off_a_scale = off;
   if (s->a_type != FKL_I8) off = align256(off + static_cast<size_t>(s->M) * 4);
   p->off_b = off;

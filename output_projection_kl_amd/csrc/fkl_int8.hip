@@ -404,9 +404,16 @@ __global__ __launch_bounds__(kSkinnyThreads) void k_project_skinny(ProjectParams
 // does not matter.
 constexpr int kIntStageK = 128;
 
-template <int TM_, int TN_, int WM_, int WN_, int S_>
+template <int TM_, int TN_, int WM_, int WN_, int S_, ProjectRead READ_ = kReadPlain>
 struct IntTile {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, S = S_;
+  template <ProjectRead READ>
+  using As = IntTile<TM, TN, WM, WN, S, READ>;
+  // B's rows by whole lines: stage t of a row starts at the line boundary at or
+  // below its 128 t-th byte, and step t lies in stages t and t + 1
+  static constexpr bool kByLines = READ_ == kReadOnceByLines;
+  static constexpr int kPolicy = READ_ == kReadPlain ? 0 : 2;  // of B's load instructions: 2 = non-temporal
+  static constexpr int kAhead = kByLines ? 2 : 1;               // stages in LDS from a step's first one on
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int XA = TM / WM / 16;  // 16-row fragments of a wave
@@ -420,6 +427,7 @@ struct IntTile {
   static constexpr bool kSpare = LA * kWaves * 8 != TM || LB * kWaves * 8 != TN;
   static constexpr int kRing = S * kStage + (kSpare ? 1024 * kWaves : 0);
   static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0, "whole fragments");
+  static_assert(S > kAhead, "a stage to load while those are used");
   // the epilogue's staging: rows of out_cols columns of the output type, 16 bytes apart from each other
   static constexpr int out_cols(int size) { return TN * size < 512 ? TN : 512 / size; }
   static constexpr int out_pitch(int size) { return out_cols(size) * size + 16; }
@@ -435,11 +443,19 @@ struct IntSrc {
   const int8_t* base;
   int32_t bytes;  // of the rows inside the operand; what lies past them reads as zero
   uint32_t off[L];
-  int32_t chunk;  // first byte of the lane's chunk within the stage
+  int32_t lead[L];  // bytes of the row's stage 0 in front of the row
+  int32_t chunk;    // first byte of the lane's chunk within the stage
   int32_t k_lim;
 };
 
-template <int R, int L>
+// Bytes from the line boundary at or below row r's start up to it: the same
+// for r and r + 16, since the rows' stride is a multiple of 16 bytes.
+__device__ __forceinline__ int line_lead(const Operand& op, int64_t row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(op.base) + static_cast<uint64_t>(row * op.ld * 2)) &
+                          (kIntStageK - 1));
+}
+
+template <int R, int L, bool LINES>
 __device__ __forceinline__ IntSrc<L> int_src(const Operand& op, int64_t row0, int wave, int lane) {
   IntSrc<L> s;
   const OperandView v = plain_view(op, row0, R);
@@ -449,6 +465,7 @@ __device__ __forceinline__ IntSrc<L> int_src(const Operand& op, int64_t row0, in
   for (int j = 0; j < L; ++j) {
     const int r = (wave * L + j) * 8 + (lane >> 3);
     s.off[j] = r < R ? static_cast<uint32_t>(r * op.ld * 2) : kOob;
+    s.lead[j] = LINES ? line_lead(op, row0 + r) : 0;
   }
   s.chunk = (lane & 7) << 4;
   s.k_lim = static_cast<int32_t>(op.k_lim) * 2;
@@ -457,7 +474,7 @@ __device__ __forceinline__ IntSrc<L> int_src(const Operand& op, int64_t row0, in
 
 // Issues stage kt of one operand into its LDS region; every lane reads out of
 // range (zeros, no memory access) where live is false.
-template <int R, int L>
+template <int R, int L, int POLICY>
 __device__ __forceinline__ void issue_int(const IntSrc<L>& s, int kt, bool live, char* region, char* spare, int wave,
                                           int lane) {
   const __amdgpu_buffer_rsrc_t rsrc =
@@ -466,11 +483,11 @@ __device__ __forceinline__ void issue_int(const IntSrc<L>& s, int kt, bool live,
   for (int j = 0; j < L; ++j) {
     const int block = wave * L + j;
     const int r = block * 8 + (lane >> 3);
-    const int k = kt * kIntStageK + (s.chunk ^ (((r >> 1) & 7) << 4));
+    const int k = kt * kIntStageK + (s.chunk ^ (((r >> 1) & 7) << 4)) - s.lead[j];
     uint32_t off = s.off[j] + static_cast<uint32_t>(k);
-    if (!live || k >= s.k_lim || s.off[j] == kOob) off = kOob;
+    if (!live || k < 0 || k >= s.k_lim || s.off[j] == kOob) off = kOob;
     char* dst = block * 8 < R ? region + block * 1024 : spare + wave * 1024;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (FKL_LDS void*)dst, 16, static_cast<int>(off), 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (FKL_LDS void*)dst, 16, static_cast<int>(off), 0, 0, POLICY);
   }
 }
 
@@ -502,13 +519,23 @@ __device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B
   const int am = (wave / C::WN) * (C::XA * 16);
   const int bn = (wave % C::WN) * (C::XB * 16);
   const int n_stages = (K + kIntStageK - 1) / kIntStageK;
-  const IntSrc<C::LA> sa = int_src<C::TM, C::LA>(A, m0, wave, lane);
-  const IntSrc<C::LB> sb = int_src<C::TN, C::LB>(B, n0, wave, lane);
+  const IntSrc<C::LA> sa = int_src<C::TM, C::LA, false>(A, m0, wave, lane);
+  const IntSrc<C::LB> sb = int_src<C::TN, C::LB, C::kByLines>(B, n0, wave, lane);
+  // of step kk: this lane's place in the stage that holds it, and which that is
+  int b_at[2];
+  bool b_next[2];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const int r = lane & 15;
+    const int at = kk * 64 + (lane >> 4) * 16 + line_lead(B, n0 + r);
+    b_at[kk] = C::kStageA + (bn + r) * kIntStageK + (((at >> 4) & 7) ^ ((r >> 1) & 7)) * 16;
+    b_next[kk] = at >= kIntStageK;
+  }
   char* const spare = lds + S * C::kStage;
   auto issue = [&](int kt) {
     char* place = lds + (kt % S) * C::kStage;
-    issue_int<C::TM, C::LA>(sa, kt, kt < n_stages, place, spare, wave, lane);
-    issue_int<C::TN, C::LB>(sb, kt, kt < n_stages, place + C::kStageA, spare, wave, lane);
+    issue_int<C::TM, C::LA, 0>(sa, kt, kt < n_stages, place, spare, wave, lane);
+    issue_int<C::TN, C::LB, C::kPolicy>(sb, kt, kt < n_stages + C::kByLines, place + C::kStageA, spare, wave, lane);
   };
   struct Set {
     i32x4 a[C::XA], b[C::XB];
@@ -518,7 +545,14 @@ __device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B
 #pragma unroll
     for (int x = 0; x < C::XA; ++x) t.a[x] = int_frag(st, am + x * 16, kk, lane);
 #pragma unroll
-    for (int y = 0; y < C::XB; ++y) t.b[y] = int_frag(st + C::kStageA, bn + y * 16, kk, lane);
+    for (int y = 0; y < C::XB; ++y) {
+      if constexpr (C::kByLines) {
+        const char* const at = b_next[kk] ? lds + ((kt + 1) % S) * C::kStage : st;
+        t.b[y] = *reinterpret_cast<const i32x4*>(at + b_at[kk] + y * 16 * kIntStageK);
+      } else {
+        t.b[y] = int_frag(st + C::kStageA, bn + y * 16, kk, lane);
+      }
+    }
   };
   auto mma = [&](const Set& t) {
 #pragma unroll
@@ -533,7 +567,7 @@ __device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B
     for (int y = 0; y < C::XB; ++y) acc[x][y] = i32x4{0, 0, 0, 0};
 #pragma unroll
   for (int p = 0; p < S; ++p) issue(p);
-  wait_vmcnt<(S - 1) * C::kDma>();
+  wait_vmcnt<(S - C::kAhead) * C::kDma>();
   block_barrier();
   read(f[0], 0, 0);
   constexpr int kMfma = C::XA * C::XB;
@@ -550,7 +584,7 @@ __device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B
       __builtin_amdgcn_sched_group_barrier(0x008, kFirst, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<(S - 2) * C::kDma>();
+    wait_vmcnt<(S - 1 - C::kAhead) * C::kDma>();
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
     block_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -706,6 +740,7 @@ using Tile128x256 = IntTile<128, 256, 2, 4, 3>;
 using Tile128 = IntTile<128, 128, 2, 2, 2>;
 using Tile64x128 = IntTile<64, 128, 2, 2, 3>;
 using Tile64 = IntTile<64, 64, 2, 2, 3>;
+using Tile32x64 = IntTile<32, 64, 1, 4, 4>;
 using Tile16x64 = IntTile<16, 64, 1, 4, 4>;
 
 template <class T, class C>
@@ -732,23 +767,32 @@ static void launch_skinny(ProjectParams P, hipStream_t st) {
     hipLaunchKernelGGL((k_project_skinny<T, 8>), grid, block, 0, st, P, static_cast<int>(ceil_div(per_wave, 8)));
 }
 
+template <class T, class C>
+static void launch_read(ProjectRead read, const ProjectParams& P, hipStream_t st) {
+  if constexpr (C::TM <= kProjectLinesRows)
+    if (read == kReadOnceByLines) return launch_tiles<T, typename C::template As<kReadOnceByLines>>(P, st);
+  if (read == kReadOnce) return launch_tiles<T, typename C::template As<kReadOnce>>(P, st);
+  launch_tiles<T, C>(P, st);
+}
+
 template <class T>
-static void launch_shape(ProjectShapeId id, const ProjectParams& P, hipStream_t st) {
-  switch (id) {
+static void launch_shape(const ProjectPlan& p, ProjectRead read, const ProjectParams& P, hipStream_t st) {
+  switch (p.shape) {
     case kProjectSkinny: return launch_skinny<T>(P, st);
-    case kProject16x64: return launch_tiles<T, Tile16x64>(P, st);
+    case kProject16x64: return launch_read<T, Tile16x64>(read, P, st);
+    case kProject32x64: return launch_read<T, Tile32x64>(read, P, st);
     case kProject64: return launch_tiles<T, Tile64>(P, st);
-    case kProject64x128: return launch_tiles<T, Tile64x128>(P, st);
+    case kProject64x128: return launch_read<T, Tile64x128>(read, P, st);
     case kProject128: return launch_tiles<T, Tile128>(P, st);
-    case kProject128x256: return launch_tiles<T, Tile128x256>(P, st);
+    case kProject128x256: return launch_read<T, Tile128x256>(read, P, st);
     case kProject256x128: return launch_tiles<T, Tile256x128>(P, st);
-    case kProject256: return launch_tiles<T, Tile256>(P, st);
+    case kProject256: return launch_read<T, Tile256>(read, P, st);
   }
 }
 
 template <class T>
-static void launch_product(const ProjectPlan& p, ProjectParams P, char* ws, hipStream_t st) {
-  if (p.splits == 1) return launch_shape<T>(p.shape, P, st);
+static void launch_product(const ProjectPlan& p, ProjectRead read, ProjectParams P, char* ws, hipStream_t st) {
+  if (p.splits == 1) return launch_shape<T>(p, read, P, st);
   // sums of each split, then their join; only the 64 x 64 tiles are split
   ProjectParams Q = P;
   int32_t* const sums = reinterpret_cast<int32_t*>(ws + p.off_sums);
@@ -784,9 +828,9 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   if (p.a_type != FKL_I8) {
     int8_t* q = reinterpret_cast<int8_t*>(g.ws + p.off_a);
     float* s = reinterpret_cast<float*>(g.ws + p.off_a_scale);
-    const hipError_t e = launch_quantize(p.M, p.K, p.a_type, g.a, p.lda, q, row16, s, st);
+    const hipError_t e = launch_quantize(p.M, p.K, p.a_type, g.a, p.lda, q, p.row_a, s, st);
     if (e != hipSuccess) return e;
-    a = q, lda = row16, a_scale = s;
+    a = q, lda = p.row_a, a_scale = s;
   } else if (p.a_copied) {
     int8_t* c = reinterpret_cast<int8_t*>(g.ws + p.off_a);
     copy(a, lda, p.M, c);
@@ -818,12 +862,18 @@ hipError_t launch_project(const ProjectPlan& p, const ProjectArgs& g, hipStream_
   const double flops = 2.0 * p.M * static_cast<double>(p.N) * p.K;
   const double bytes = static_cast<double>(p.M) * p.K + static_cast<double>(p.N) * p.K +
                        static_cast<double>(p.M) * p.N * type_bytes(p.out_type);
-  static const char* const kNames[] = {"project_16x16",   "project_16x64",   "project_64x64",   "project_64x128",
-                                       "project_128x128", "project_128x256", "project_256x128", "project_256x256"};
+  const bool at_lines = ldb % 128 == 0 && reinterpret_cast<uintptr_t>(b) % 128 == 0;
+  const ProjectRead read = !p.once ? kReadPlain
+                           : at_lines ? kReadOnce
+                           : p.shape <= kProject32x64 ? kReadOnceByLines
+                                                      : kReadPlain;
+  static const char* const kNames[] = {"project_16x16",   "project_16x64",   "project_32x64",   "project_64x64",
+                                       "project_64x128",  "project_128x128", "project_128x256", "project_256x128",
+                                       "project_256x256"};
   TraceScope ts(st, p.splits > 1 ? "project_split" : kNames[p.shape], flops, bytes);
-  if (p.out_type == FKL_F32) launch_product<float>(p, P, g.ws, st);
-  else if (p.out_type == FKL_BF16) launch_product<__bf16>(p, P, g.ws, st);
-  else launch_product<_Float16>(p, P, g.ws, st);
+  if (p.out_type == FKL_F32) launch_product<float>(p, read, P, g.ws, st);
+  else if (p.out_type == FKL_BF16) launch_product<__bf16>(p, read, P, g.ws, st);
+  else launch_product<_Float16>(p, read, P, g.ws, st);
   return hipGetLastError();
 }
 

@@ -133,6 +133,7 @@ def test_project_int8_rows(M, N, K, out):
 # One size and more for every layout of the product, under the names of the
 # library's trace; ragged in every dimension.
 LAYOUTS = [(5, 70, 500, "project_16x16"), (85, 706, 417, "project_16x16"), (9, 30001, 1000, "project_16x64"),
+           (25, 30001, 1000, "project_32x64"),
            (60, 40001, 1030, "project_64x64"), (38, 56217, 335, "project_64x128"), (117, 31149, 1090, "project_128x128"),
            (139, 19627, 2383, "project_128x256"), (201, 32003, 2887, "project_256x128"),
            (1030, 20003, 700, "project_256x256"), (505, 323, 7071, "project_split"), (3, 16, 9000, "project_split"),
@@ -260,3 +261,39 @@ def test_project_uses_the_given_workspace_and_stream(M):
     assert torch.equal(out, want) and (ws[need:] == 255).all()
     with pytest.raises(ValueError):
         fkl.project(a, b, sb, out=out, workspace=ws[:need - 1])
+
+
+# A head larger than the last-level cache is read once, by hints or by whole
+# lines, in tiles that follow the rows: the same sums as those of its parts,
+# which are small enough to be read otherwise. Rows that start at every multiple
+# of 16 bytes of a 128-byte line, alike and each its own; one stage and several,
+# with every remainder of the last one.
+@pytest.mark.parametrize("M,N,K,ldb,first", [
+    (1, 120011, 2304, 2304, 0), (16, 140003, 1921, 1936, 16), (9, 2500003, 100, 112, 0), (2, 2200019, 128, 128, 48),
+    (17, 101009, 2880, 2880, 64), (32, 110017, 2500, 2560, 112), (31, 130003, 2177, 2192, 32), (29, 2400011, 112, 112, 96),
+    (64, 120011, 2304, 2304, 0), (40, 100003, 2880, 2880, 0), (65, 100003, 2816, 2816, 0), (128, 100003, 2833, 2848, 80),
+    (129, 95003, 2944, 2944, 0), (250, 100003, 2700, 2704, 0)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_project_heads_larger_than_the_cache(M, N, K, ldb, first, out):
+    dev = _dev()
+    g = torch.Generator(device=dev).manual_seed(M + N + K)
+    store = torch.empty(N * ldb + 256, dtype=torch.int8, device=dev)
+    store.random_(-128, 128, generator=g)
+    assert N * ldb > 1 << 28 and store.data_ptr() % 128 == 0
+    b = torch.as_strided(store, (N, K), (ldb, 1), first)
+    a = torch.randint(-128, 128, (M, -(-K // 16) * 16), generator=g, dtype=torch.int8, device=dev)[:, :K]
+    sa = torch.rand(M, generator=g, device=dev)
+    sb = torch.rand(N, generator=g, device=dev)
+    got = fkl.project(a, b, sb, a_scale=sa, out_dtype=out)
+    part = (200 << 20) // ldb  # rows
+    for n in range(0, N, part):
+        want = fkl.project(a, b[n:n + part], sb[n:n + part], a_scale=sa, out_dtype=out)
+        assert torch.equal(got[:, n:n + part], want), (n, N)
+    # and some columns from the formula
+    at = torch.randint(0, N, (64,), generator=g, device=dev)
+    at[0], at[1] = 0, N - 1
+    exact = (a.double() @ b[at].double().T).to(torch.float32) * sa[:, None]
+    want = (exact.double() * sb[at].double()).float().to(out)
+    err = (got[:, at].double() - want.double()).abs()
+    # the same roundings to fp32 and to out: at most a step of out apart
+    assert (err <= want.double().abs() * torch.finfo(out).eps).all()
