@@ -28,6 +28,8 @@ enum DecodeDebugBit : uint32_t {
 };
 constexpr int kDecodeDebugBits = 6;
 
+constexpr int64_t kLastLevelBytes = int64_t(256) << 20;  // of cache between the L2s and memory
+
 // How the product is laid out on the GPU: the split-contraction kernel for few
 // output elements, or block tiles.
 enum ProjectShapeId {

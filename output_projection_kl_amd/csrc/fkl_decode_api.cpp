@@ -79,6 +79,8 @@ fkl_status debug_end(char* ws, hipStream_t stream) {
 
 namespace fkl {
 
+// The layout of the product.
+//
 // A b larger than the last-level cache is not there at the next call. For up
 // to 256 rows it is read once, memory decides, and its loads say so (they are
 // non-temporal): 128256 x 4096 rows, 85 instead of 99 us for 8 rows of a, 91
@@ -89,9 +91,8 @@ namespace fkl {
 // read by whole lines (up to 32 rows of a: 201088 x 2880, 101 instead of 115 us
 // for 16, 111 instead of 122 for 32), or without the hint (48: 129 us, 134 by
 // whole lines, 144 with the hint alone).
-constexpr int64_t kLastLevelBytes = int64_t(256) << 20;
-
-// The layout with the least estimated time, us. A block tile's stage (128
+//
+// Otherwise the layout with the least estimated time, us. A block tile's stage (128
 // bytes of the contraction) takes `filled` of a CU that as many workgroups
 // share as fit, and `alone` for a workgroup with a CU to itself, whichever is
 // longer over the rounds that the tiles take; then the tile is stored. The

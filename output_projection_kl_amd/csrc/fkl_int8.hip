@@ -137,7 +137,7 @@ __device__ __forceinline__ void pack_levels(const typename QuantOf<T>::Scale& s,
 // One workgroup per row, in pieces of 16 bytes of x; the row's last few
 // elements one by one. Pieces are read and written at any alignment (the GPU
 // splits an access that crosses a line).
-template <class T>
+template <class T, bool ONCE>
 __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict__ x, int64_t ldx, int cols,
                                                             int8_t* __restrict__ q, int64_t ldq,
                                                             float* __restrict__ scale) {
@@ -146,18 +146,18 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict_
   constexpr int kHeld = kQuantHeldBytes / 16;
   constexpr int kWords = kPer / 4;
   typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
-  struct __attribute__((packed)) AnyPiece {
-    u32x4 v;
-  };
-  struct __attribute__((packed)) AnyWords {
-    Words v;
-  };
+  typedef u32x4 AnyPiece __attribute__((aligned(1)));
+  typedef Words AnyWords __attribute__((aligned(1)));
   const int64_t row = blockIdx.x;
   const T* const src = x + row * ldx;
   int8_t* const dst = q + row * ldq;
   const int n = cols / kPer;
   const int tail = n * kPer + threadIdx.x;  // this thread's element of the tail
-  auto get = [&](int i) { return reinterpret_cast<const AnyPiece*>(src + static_cast<int64_t>(i) * kPer)->v; };
+  auto get = [&](int i) -> u32x4 {
+    const AnyPiece* const at = reinterpret_cast<const AnyPiece*>(src + static_cast<int64_t>(i) * kPer);
+    if constexpr (ONCE) return __builtin_nontemporal_load(at);
+    else return *at;
+  };
   auto element = [&](int i) -> uint32_t {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(uint32_t, src[i]);
     else return __builtin_bit_cast(uint16_t, src[i]);
@@ -190,7 +190,9 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict_
     Words out;
 #pragma unroll
     for (int j = 0; j < kWords; ++j) out[j] = zero ? 0u : w[j];
-    reinterpret_cast<AnyWords*>(dst + static_cast<int64_t>(i) * kPer)->v = out;
+    AnyWords* const at = reinterpret_cast<AnyWords*>(dst + static_cast<int64_t>(i) * kPer);
+    if constexpr (ONCE) __builtin_nontemporal_store(out, at);
+    else *at = out;
   };
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
@@ -205,8 +207,11 @@ template <class T>
 static void launch_quantize_of(int64_t rows, int64_t cols, const void* x, int64_t ldx, int8_t* q, int64_t ldq,
                                float* scale, hipStream_t st) {
   constexpr int64_t kRowsPerLaunch = int64_t(1) << 23;  // grid x block stays below 2^32 threads
+  // what the last-level cache cannot keep is better not brought there
+  const int64_t bytes = rows * cols * static_cast<int64_t>(sizeof(T));
+  auto* const k = bytes > kLastLevelBytes ? k_quantize<T, true> : k_quantize<T, false>;
   for (int64_t r = 0; r < rows; r += kRowsPerLaunch)
-    hipLaunchKernelGGL(k_quantize<T>, dim3(static_cast<unsigned>(std::min(rows - r, kRowsPerLaunch))),
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(std::min(rows - r, kRowsPerLaunch))),
                        dim3(kQuantThreads), 0, st, static_cast<const T*>(x) + r * ldx, ldx, static_cast<int>(cols),
                        q + r * ldq, ldq, scale + r);
 }

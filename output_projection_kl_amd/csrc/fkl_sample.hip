@@ -531,14 +531,17 @@ struct RowView {
   // Pieces i0 + tid + b * stride, b < N, for a block of `stride` threads: all
   // inside the row but for the first and last such batches, which alone look at
   // every piece (a load behind a branch of its own waits there).
-  template <int N>
+  // ONCE: with the hint that they are not asked for again.
+  template <int N, bool ONCE = false>
   __device__ __forceinline__ void batch(const DebugCheck& dbg, int i0, int stride, u32x4 (&v)[N]) const {
     const int first = i0 + static_cast<int>(threadIdx.x);
     if (i0 * kPer - lead >= 0 && (i0 + N * stride) * kPer - lead <= V) {
 #pragma unroll
-      for (int b = 0; b < N; ++b)
-        v[b] = dload(dbg, 0, kDbgSampleLogits,
-                     reinterpret_cast<const u32x4*>(x + ((first + b * stride) * kPer - lead)));
+      for (int b = 0; b < N; ++b) {
+        const u32x4* const at = reinterpret_cast<const u32x4*>(x + ((first + b * stride) * kPer - lead));
+        if constexpr (!ONCE) v[b] = dload(dbg, 0, kDbgSampleLogits, at);
+        else v[b] = dcheck_range(dbg, 0, kDbgSampleLogits, at, 16) ? __builtin_nontemporal_load(at) : u32x4{0, 0, 0, 0};
+      }
     } else {
 #pragma unroll
       for (int b = 0; b < N; ++b) v[b] = raw(dbg, first + b * stride);
@@ -597,7 +600,7 @@ __device__ __forceinline__ uint64_t hist_word(const EighthSeries& power, const E
 // wanted; with the masses, one fp64 exponential per entry (about 20 vector
 // instructions, and an LDS atomic for the histogram) takes longer than the
 // reading.
-template <class T, int kThreads>
+template <class T, int kThreads, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   constexpr int kPer = RowView<T>::kPer;
   constexpr int kPieces = kScanElems / kPer;
@@ -613,7 +616,7 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   const RowView<T> view(P, row);
   const int64_t slot = row * P.chunks + chunk;
   u32x4 held[kPieces];
-  view.template batch<kPieces>(P.dbg, chunk * (kThreads * kPieces), kThreads, held);
+  view.template batch<kPieces, ONCE>(P.dbg, chunk * (kThreads * kPieces), kThreads, held);
   float x[kPieces][kPer];
 #pragma unroll
   for (int p = 0; p < kPieces; ++p)
@@ -1709,9 +1712,11 @@ static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hip
       TraceScope ts(st, "sample_scan", 0.0, bytes);
       const dim3 grid(static_cast<unsigned>(rows * p.chunks));
       if (p.chunk_elems == 256 * kScanElems)
-        hipLaunchKernelGGL((k_sample_scan<T, 256>), grid, dim3(256), 0, st, P);
+        hipLaunchKernelGGL((k_sample_scan<T, 256, false>), grid, dim3(256), 0, st, P);
+      else if (bytes > kLastLevelBytes)
+        hipLaunchKernelGGL((k_sample_scan<T, 1024, true>), grid, dim3(1024), 0, st, P);
       else
-        hipLaunchKernelGGL((k_sample_scan<T, 1024>), grid, dim3(1024), 0, st, P);
+        hipLaunchKernelGGL((k_sample_scan<T, 1024, false>), grid, dim3(1024), 0, st, P);
     }
     TraceScope ts(st, "sample_pick", 0.0, 4.0 * p.N * p.groups);
     hipLaunchKernelGGL(k_sample_pick<T>, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st, P, shift);
