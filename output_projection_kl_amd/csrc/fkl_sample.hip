@@ -23,11 +23,14 @@
 //     equal logits, thousands of entries kept by top-k): sample_row_exact, one
 //     workgroup per row, radix selection over the row itself.
 #include <algorithm>
+#include <type_traits>
 
 #include "fkl_decode.h"
 #include "fkl_device.h"
 
 namespace fkl {
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
@@ -526,6 +529,15 @@ struct RowView {
       else v[j / 2] = __builtin_bit_cast(uint16_t, e);
     }
     return v;
+  }
+
+  __device__ __forceinline__ bool is_whole(int i) const { return i * kPer >= lead && (i + 1) * kPer - lead <= V; }
+
+  // Piece i where all of it is inside the row, some other one where it is not
+  // (read in any case: no branch to wait in).
+  __device__ __forceinline__ u32x4 whole(const DebugCheck& dbg, int i) const {
+    const int in = min(max(i, (lead + kPer - 1) / kPer), (lead + V) / kPer - 1);
+    return dload(dbg, 0, kDbgSampleLogits, reinterpret_cast<const u32x4*>(x + (in * kPer - lead)));
   }
 
   // Pieces i0 + tid + b * stride, b < N, for a block of `stride` threads: all
@@ -1149,6 +1161,11 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
   return true;
 }
 
+// Keys of 16-bit logits differ in their upper bits alone: a bin of 2^GRAIN keys,
+// aligned to that, holds one of them.
+template <class T>
+constexpr int kGrain = std::is_same<T, __bf16>::value ? 16 : std::is_same<T, _Float16>::value ? 13 : 0;
+
 // The last entry kept of a list in LDS: the last, in the order of (key
 // descending, position ascending), before which the entries of keys in [lo,
 // hi) amount to less than `target`: their number, or the units of their
@@ -1158,16 +1175,17 @@ __device__ __forceinline__ bool row_histogram(const SampleParams& P, int64_t slo
 // again, until that bin holds at most 64 entries, which one wave compares, or
 // entries of one key, of which the last one's position is looked for among as
 // many bins of positions. Returns the entry to every thread.
-template <class Entry, class Units>
+template <int GRAIN, class Entry, class Units>
 __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint32_t lo, uint64_t hi, bool by_units,
                                                  uint64_t target, Entry entry, Units units) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   uint64_t above = 0;
   int count;
+  lo &= ~((1u << GRAIN) - 1);
   for (;;) {
     const uint32_t span = static_cast<uint32_t>(hi - lo - 1);
-    const int shift = max(0, 32 - kFineBits - __clz(static_cast<int>(span | 1)));
+    const int shift = max(GRAIN, 32 - kFineBits - __clz(static_cast<int>(span | 1)));
     __syncthreads();
     L.fine.count[tid] = 0;
     L.fine.units[tid] = 0;
@@ -1200,7 +1218,7 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
     above = L.units;
     lo += static_cast<uint32_t>(kRowThreads - 1 - at) << shift;
     hi = min(hi, static_cast<uint64_t>(lo) + (uint64_t(1) << shift));
-    if (count <= 64 || shift == 0) break;
+    if (count <= 64 || shift == GRAIN) break;
   }
   L.few[lane] = 0;
   if (tid == 0) L.word[7] = 0;
@@ -1223,6 +1241,8 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
       if (lane == 0) L.edge = last;
     }
   } else {
+    // the key whose bin it is: positive logits' lower bits are 0, negative ones' 1
+    if (!(lo & 0x80000000u)) lo |= (1u << GRAIN) - 1;
     const uint64_t each = by_units ? max(units(lo), uint64_t(1)) : 1;
     const uint64_t want = (target - above + each - 1) / each;  // >= 1
     const uint32_t quota = static_cast<uint32_t>(min(want, static_cast<uint64_t>(count)));
@@ -1250,25 +1270,52 @@ __device__ __forceinline__ uint64_t border_entry(PickLds& L, int V, int n, uint3
       }
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t nth = L.word[9], pos = pos_bin << pos_shift;
-      for (int i = 0; i < 64; ++i) {
-        uint32_t bits = L.few[i];
-        const uint32_t c = static_cast<uint32_t>(__popc(bits));
-        if (nth > c) {
-          nth -= c;
-          continue;
-        }
-        while (--nth > 0) bits &= bits - 1;
-        pos += static_cast<uint32_t>(i * 32 + __ffs(static_cast<int>(bits)) - 1);
-        break;
+    if (tid < 64) {
+      uint32_t bits = L.few[lane];
+      const uint32_t c = static_cast<uint32_t>(__popc(bits));
+      const uint32_t before_c = wave_scan(c) - c;
+      uint32_t nth = L.word[9];
+      if (before_c < nth && before_c + c >= nth) {
+        while (--nth > before_c) bits &= bits - 1;
+        const uint32_t pos = (pos_bin << pos_shift) + static_cast<uint32_t>(lane * 32 + __ffs(static_cast<int>(bits)) - 1);
+        L.edge = (static_cast<uint64_t>(lo) << 32) | ~pos;
       }
-      L.edge = (static_cast<uint64_t>(lo) << 32) | ~pos;
     }
   }
   __syncthreads();
   return L.edge;
 }
+
+// Elements of a 16-bit type in [x_lo, x_hi), two at a time, where the range
+// does not reach zero: their bits are consecutive there, the magnitudes rising.
+template <class T>
+struct Range16 {
+  bool one_sign;
+  uint32_t first, count;  // twice in a word
+  // the least bits of a magnitude that is at least y, or larger than y
+  static __device__ __forceinline__ uint32_t least(float y, bool larger) {
+    if constexpr (sizeof(T) == 2) {
+      const T t = static_cast<T>(y);  // the nearest: its neighbour below is too small
+      const float v = static_cast<float>(t);
+      return __builtin_bit_cast(uint16_t, t) + (v < y || (larger && v == y) ? 1u : 0u);
+    }
+    return 0;
+  }
+  __device__ __forceinline__ Range16(float x_lo, float x_hi) {
+    one_sign = x_lo > 0.0f || x_hi < 0.0f;
+    const bool minus = x_hi < 0.0f;
+    const uint32_t a = minus ? least(-x_hi, true) : least(x_lo, false);
+    const uint32_t b = minus ? least(-x_lo, true) : least(x_hi, false);
+    first = (a | (minus ? 0x8000u : 0u)) * 0x10001u;
+    count = (b - a) * 0x10001u;
+  }
+  // 1 in each half of the word whose element is in the range
+  __device__ __forceinline__ uint32_t inside(uint32_t word) const {
+    const u16x2 from = __builtin_bit_cast(u16x2, word) - __builtin_bit_cast(u16x2, first);
+    const u16x2 left = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, count), from);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(left, u16x2{1, 1}));
+  }
+};
 
 // A row of which more entries are kept than the workgroup holds: the bins
 // above the border are kept whole, and only the border bin's entries are
@@ -1347,19 +1394,14 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
     __syncthreads();
   }
   const float x_lo = key_logit(k_lo), x_hi = key_logit(k_hi), x_end = key_logit(bin_end);
+  const Range16<T> range(x_lo, x_hi);
   for (int p0 = 0; p0 < pieces; p0 += kBatch * kRowThreads) {  // the same for all lanes: they vote below
     const int i0 = p0 + tid;
     u32x4 held[kBatch];
     view.template batch<kBatch>(P.dbg, p0, kRowThreads, held);
+    if (x_hi < x_end) {  // the bin's entries above the finer one are kept: their chunk's mass
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      uint32_t hits = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float x = view.logit(held[b], j);
-        hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << j;
-      }
-      if (x_hi < x_end) {  // the bin's entries above the finer one are kept: their chunk's mass
+      for (int b = 0; b < kBatch; ++b) {
         uint64_t kept = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -1374,23 +1416,41 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
                       static_cast<unsigned long long>(all));
         }
       }
-      if (__ballot(hits != 0) == 0) continue;
-      const uint32_t mine = static_cast<uint32_t>(__popc(hits));
-      const uint32_t incl = wave_scan(mine);
-      uint32_t at = 0;
-      if (lane == 63) at = atomicAdd(&L.word[2], incl);
-      at = from_lane(at, 63) + incl - mine;
-      const int pos = (i0 + b * kRowThreads) * kPer - view.lead;
-      for (; hits; hits &= hits - 1, ++at) {
-        const int j = __ffs(static_cast<int>(hits)) - 1;
-        float x = view.logit(held[b], 0);
+    }
+    // bit b kPer + j: element j of piece b; for 16-bit types bit 4 b + i: element 2 i, 16 more: 2 i + 1
+    uint32_t hits = 0;
+    if (sizeof(T) == 2 && range.one_sign) {
 #pragma unroll
-        for (int i = 1; i < kPer; ++i) x = i == j ? view.logit(held[b], i) : x;
-        if (at < kFlatEntries) L.entry[at] = (static_cast<uint64_t>(logit_key(x)) << 32) | ~static_cast<uint32_t>(pos + j);
-      }
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hits |= range.inside(held[b][i]) << (b * 4 + i);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const float x = view.logit(held[b], j);
+          const int bit = sizeof(T) == 2 ? b * 4 + j / 2 + j % 2 * 16 : b * kPer + j;
+          hits |= (x >= x_lo && x < x_hi ? 1u : 0u) << bit;
+        }
+    }
+    const uint32_t mine = static_cast<uint32_t>(__popc(hits));
+    const uint32_t incl = wave_scan(mine);
+    uint32_t at = 0;
+    if (lane == 63) at = atomicAdd(&L.word[2], incl);
+    at = from_lane(at, 63) + incl - mine;
+    for (; hits; hits &= hits - 1, ++at) {
+      const int bit = __ffs(static_cast<int>(hits)) - 1;
+      const int b = bit / 4 % 4, j = sizeof(T) == 2 ? bit % 4 * 2 + bit / 16 : bit % 4;
+      if (at < kFlatEntries) L.entry[at] = static_cast<uint32_t>((i0 + b * kRowThreads) * kPer + j - view.lead);
     }
   }
-  const uint64_t edge = border_entry(L, V, n, k_lo, k_hi, !by_count, target, [&](int i) { return L.entry[i]; }, units);
+  __syncthreads();
+  for (int i = tid; i < n; i += kRowThreads) {
+    const uint32_t pos = static_cast<uint32_t>(L.entry[i]);
+    L.entry[i] = (static_cast<uint64_t>(view.element(P.dbg, static_cast<int>(pos) + view.lead)) << 32) | ~pos;
+  }
+  const uint64_t edge = border_entry<kGrain<T>>(L, V, n, k_lo, k_hi, !by_count, target, [&](int i) { return L.entry[i]; }, units);
   const uint32_t edge_key = static_cast<uint32_t>(edge >> 32);
   const int edge_pos = static_cast<int>(~static_cast<uint32_t>(edge));
   // each chunk's kept mass: its bins above the border, and its kept entries of the border bin
@@ -1407,10 +1467,14 @@ __device__ __forceinline__ bool pick_flat_row(const SampleParams& P, int64_t row
   for (int ch = wave; ch < P.chunks; ch += kRowWaves) {
     const int off = L.chunk_off[ch];
     double s = 0.0;
-#pragma unroll 4
-    for (int d = lane; d < border - off; d += 64) {
-      const uint64_t w = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + d);
-      s += units_mass(hist_units(w)) * L.bin_scale[off + d];
+    uint64_t w[kScanBins / 64];  // read before any is used, and in any case: no branch to wait in
+#pragma unroll
+    for (int i = 0; i < kScanBins / 64; ++i)
+      w[i] = dload(P.dbg, 5, kDbgSampleWork, P.chunk_hist + (slot + ch) * kScanBins + i * 64 + lane);
+#pragma unroll
+    for (int i = 0; i < kScanBins / 64; ++i) {
+      const int d = i * 64 + lane;
+      if (d < border - off) s += units_mass(hist_units(w[i])) * L.bin_scale[off + d];
     }
     s = wave_sum_f64(s);
     if (lane == 0) L.chunk[ch] = s + static_cast<double>(L.chunk_units[ch]) * scale;
@@ -1503,63 +1567,47 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
       if (L.group_max[g] >= bound) L.list[at++] = static_cast<uint32_t>(g);
   }
   __syncthreads();
-  // a wave reads 64 entries at a time: one group of 64, or four of 16
-  const int shift = P.group_shift;
-  const int steps = ((static_cast<int>(n_list) << shift) + 63) >> 6;
-  const int per_wave = (steps + kRowWaves - 1) / kRowWaves;
-  const int l0 = min(wave * per_wave, steps);
-  const int l1 = min(l0 + per_wave, steps);
-  auto element_of = [&](int l) {  // this lane's element of step l, -1 past the list
-    const int i = (l * 64 + lane) >> shift;
-    return i < static_cast<int>(n_list) ? static_cast<int>(L.list[i] << shift) + (lane & ((1 << shift) - 1)) : -1;
-  };
-  auto key_of = [&](int l) { return view.element(P.dbg, element_of(l)); };
-  // steps read before any is used; the first batch is held for the second round
-  constexpr int kBatch = 8;
-  uint32_t first[kBatch];
-  auto read = [&](int l, uint32_t (&key)[kBatch]) {
+  // Each thread reads a run of kRun pieces of the listed groups and appends the
+  // entries that reach the bound behind those of the threads before it.
+  constexpr int kPer = RowView<T>::kPer;
+  constexpr int kRun = 4;
+  const float bound_x = key_logit(bound);
+  const int shift = P.group_shift - (kPer == 8 ? 3 : 2);  // pieces of a group
+  const int pieces = static_cast<int>(n_list) << shift;
+  uint32_t n_cand = 0;
+  for (int p0 = 0, turn = 0; p0 < pieces; p0 += kRun * kRowThreads, turn ^= 1) {
+    u32x4 held[kRun];
+    int piece[kRun];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const uint32_t k = key_of(l + b);
-      key[b] = l + b < l1 ? k : 0u;
+    for (int r = 0; r < kRun; ++r) {
+      const int i = p0 + tid * kRun + r;
+      piece[r] = i < pieces ? static_cast<int>(L.list[i >> shift] << shift) + (i & ((1 << shift) - 1)) : -1;
     }
-  };
-  read(l0, first);
-  uint32_t found = 0;
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(first[b] >= bound));
-  for (int l = l0 + kBatch; l < l1; l += kBatch) {
-    uint32_t key[kBatch];
-    read(l, key);
+    for (int r = 0; r < kRun; ++r) held[r] = view.whole(P.dbg, piece[r]);
+    uint32_t hits[kRun], mine = 0, sum;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) found += __popcll(__ballot(key[b] >= bound));
-  }
-  if (lane == 0) L.wave_u32[5][wave] = found;
-  __syncthreads();
-  uint32_t put = 0, n_cand = 0;
+    for (int r = 0; r < kRun; ++r) {
+      if (!view.is_whole(piece[r]) && piece[r] >= 0) held[r] = view.raw(P.dbg, piece[r]);  // the row's first and last
+      hits[r] = 0;
 #pragma unroll
-  for (int w = 0; w < kRowWaves; ++w) {
-    if (w == wave) put = n_cand;
-    n_cand += L.wave_u32[5][w];
-  }
-  if (n_cand > kCandidates) return false;
-  auto keep = [&](int l, const uint32_t (&key)[kBatch]) {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const uint64_t hit = __ballot(key[b] >= bound);
-      if (key[b] >= bound) {
-        const uint32_t at = put + __popcll(hit & ((uint64_t(1) << lane) - 1));
-        L.cand.key[at] = key[b];
-        L.cand.pos[at] = element_of(l + b) - view.lead;
-      }
-      put += __popcll(hit);
+      for (int j = 0; j < kPer; ++j) hits[r] |= (view.logit(held[r], j) >= bound_x ? 1u : 0u) << j;
+      if (piece[r] < 0) hits[r] = 0;
+      mine += static_cast<uint32_t>(__popc(hits[r]));
     }
-  };
-  keep(l0, first);
-  for (int l = l0 + kBatch; l < l1; l += kBatch) {
-    uint32_t key[kBatch];
-    read(l, key);
-    keep(l, key);
+    uint32_t at = n_cand + block_scan(mine, L.wave_u32[turn ? 5 : 3], sum);
+    if (mine > 0) {
+#pragma unroll
+      for (int r = 0; r < kRun; ++r)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (((hits[r] >> j) & 1u) && at < kCandidates) {
+            L.cand.key[at] = logit_key(view.logit(held[r], j));
+            L.cand.pos[at++] = piece[r] * kPer + j - view.lead;
+          }
+    }
+    n_cand += sum;
+    if (n_cand > kCandidates) return false;
   }
   __syncthreads();
   const int n = static_cast<int>(n_cand);
@@ -1578,7 +1626,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   };
   uint64_t edge = 0;
   if (S.k < static_cast<uint32_t>(n))
-    edge = border_entry(L, V, n, bound, uint64_t(m_key) + 1, false, S.k, entry, units);
+    edge = border_entry<kGrain<T>>(L, V, n, bound, uint64_t(m_key) + 1, false, S.k, entry, units);
   if (S.p < 1.0) {
     if (whole < 0.0) {
       double s = 0.0;
@@ -1587,7 +1635,7 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
       block_scan(s, L.wave_f64[2], whole);
     }
     const uint64_t target = max(static_cast<uint64_t>(ceil(S.p * whole * kUnit)), uint64_t(1));
-    edge = max(edge, border_entry(L, V, n, bound, uint64_t(m_key) + 1, true, target, entry, units));
+    edge = max(edge, border_entry<kGrain<T>>(L, V, n, bound, uint64_t(m_key) + 1, true, target, entry, units));
   }
   // the draw: thread t holds candidates t * per .. in order of position
   constexpr int kPerThread = kCandidates / kRowThreads;
@@ -1628,8 +1676,12 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
 
 // One workgroup per row, after k_sample_scan. Latency bound: a chain of short
 // steps over LDS, with one dependent read of the groups that reach the bound.
-template <class T>
-__global__ __launch_bounds__(kRowThreads) void k_sample_pick(SampleParams P, int shift) {
+// Up to one row per CU, a workgroup's waves have all of its registers (87);
+// with more rows two workgroups share it (64 registers, some spilled): 512 rows
+// of 201088 fp32 logits, 24 instead of 32 us; 64 rows of 128256 bf16 logits 32
+// instead of 30 us.
+template <class T, int WAVES>
+__global__ __launch_bounds__(kRowThreads, WAVES) void k_sample_pick(SampleParams P, int shift) {
   __shared__ union {
     PickLds pick;
     ExactLds exact;
@@ -1689,9 +1741,10 @@ static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hip
   const int64_t per_row = p.route == kSampleScan ? p.chunks : 1;
   const int regs = static_cast<int>(ceil_div(p.V, 64));  // a short row's entries per lane
   const int64_t rows_max = std::max<int64_t>(1, (int64_t(1) << 21) / per_row);
-  const double bytes = static_cast<double>(p.N) * p.V * sizeof(T);
+  const bool once = p.N * p.V * static_cast<int64_t>(sizeof(T)) > kLastLevelBytes;
   for (int64_t r = 0; r < p.N; r += rows_max) {
     const int64_t rows = std::min(p.N - r, rows_max);
+    const double bytes = static_cast<double>(rows) * p.V * sizeof(T);
     P.row0 = r;
     if (p.route == kSampleShort) {
       auto* k = regs <= 1   ? k_sample_short<T, 1>
@@ -1713,13 +1766,14 @@ static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hip
       const dim3 grid(static_cast<unsigned>(rows * p.chunks));
       if (p.chunk_elems == 256 * kScanElems)
         hipLaunchKernelGGL((k_sample_scan<T, 256, false>), grid, dim3(256), 0, st, P);
-      else if (bytes > kLastLevelBytes)
+      else if (once)
         hipLaunchKernelGGL((k_sample_scan<T, 1024, true>), grid, dim3(1024), 0, st, P);
       else
         hipLaunchKernelGGL((k_sample_scan<T, 1024, false>), grid, dim3(1024), 0, st, P);
     }
-    TraceScope ts(st, "sample_pick", 0.0, 4.0 * p.N * p.groups);
-    hipLaunchKernelGGL(k_sample_pick<T>, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st, P, shift);
+    TraceScope ts(st, "sample_pick", 0.0, 4.0 * rows * p.groups);
+    auto* const pick = rows > kTargetBlocks ? k_sample_pick<T, 8> : k_sample_pick<T, 4>;
+    hipLaunchKernelGGL(pick, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st, P, shift);
   }
 }
 
