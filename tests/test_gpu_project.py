@@ -297,3 +297,18 @@ def test_project_heads_larger_than_the_cache(M, N, K, ldb, first, out):
     err = (got[:, at].double() - want.double()).abs()
     # the same roundings to fp32 and to out: at most a step of out apart
     assert (err <= want.double().abs() * torch.finfo(out).eps).all()
+
+
+@pytest.mark.parametrize("dtype,M,K", [(torch.bfloat16, 50021, 2881), (torch.float32, 20011, 4096)])
+def test_quantize_more_than_the_cache_holds(dtype, M, K):
+    """Rows streamed past the last-level cache: the same levels as those of their halves, which are not."""
+    dev = _dev()
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn((M, K), generator=g, device=dev).to(dtype)
+    assert x.nbytes > 1 << 28 > x.nbytes * 11 // 20
+    q, scale = fkl.quantize(x)
+    half = (M + 1) // 2
+    for r in (0, half):
+        q1, scale1 = fkl.quantize(x[r:r + half])
+        assert torch.equal(q[r:r + half], q1) and torch.equal(scale[r:r + half], scale1)
+    _check_levels(x[-70:], q[-70:], scale[-70:])

@@ -249,3 +249,38 @@ def test_sample_frequencies():
     want = np.zeros(V)
     want[pos] = w / w.sum() * n
     assert np.abs(np.bincount(token.cpu().numpy(), minlength=V) - want).max() <= 1.0
+
+
+# Rows that keep thousands of entries, their logits moved so that the border
+# lies among positive, negative and zero ones; each with as many rows as two
+# workgroups on a CU take, and with few.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [4, 258])
+@pytest.mark.parametrize("shift", [-40.0, -1.5, 0.0, 30.0])
+def test_sample_wide_borders_of_either_sign(shift, N, dtype):
+    dev = _dev()
+    V = 9001
+    g = torch.Generator().manual_seed(N + int(shift * 2))
+    x = (torch.randn((N, V), generator=g) * 1.2 + shift).to(dtype).to(dev)
+    u = torch.rand(N, generator=g).to(dev)
+    _check(x, u, p=0.8)
+    _check(x, u, T=2.0, p=0.9)
+    _check(x, u, k=3500)
+    _check(x, u, q=0.002)
+
+
+@pytest.mark.parametrize("dtype,N,V", [(torch.float32, 600, 120001), (torch.bfloat16, 1030, 150016)])
+def test_sample_logits_larger_than_the_cache(dtype, N, V):
+    """Logits that are streamed past the last-level cache: the same draws as from their halves, which are not."""
+    dev = _dev()
+    g = torch.Generator(device=dev).manual_seed(V)
+    x = (2.0 * torch.randn((N, V), generator=g, device=dev)).to(dtype)
+    u = torch.rand(N, generator=g, device=dev)
+    assert x.nbytes > 1 << 28 > x.nbytes * 11 // 20
+    half = (N + 1) // 2
+    for s in (dict(temperature=0.8), dict(top_k=40, top_p=0.9), dict(top_p=0.9), dict(top_p=0.9, min_p=0.01)):
+        token, logprob = fkl.sample(x, u, **s)
+        parts = [fkl.sample(x[r:r + half], u[r:r + half], **s) for r in (0, half)]
+        assert torch.equal(token, torch.cat([p[0] for p in parts]))
+        assert torch.allclose(logprob, torch.cat([p[1] for p in parts]), rtol=2.0 ** -22, atol=1e-11)
+    _check(x[:6], u[:6], p=0.9)
