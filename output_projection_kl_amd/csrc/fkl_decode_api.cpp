@@ -222,11 +222,13 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
   if (p->route == kSampleScan) {
     // the larger chunks where they leave enough workgroups for every CU
-    p->chunk_elems = s->N * ceil_div(s->V, kSampleChunkLarge) >= 2 * kTargetBlocks ? kSampleChunkLarge
-                                                                                   : kSampleChunkSmall;
-    // the smaller groups as long as a row has at most 4096 of them: top-k's
-    // bound, the k-th largest group maximum, needs many more groups than k
-    p->group_shift = s->V + 7 <= 4096 * 16 ? 4 : 6;
+    p->chunk_elems = s->N * ceil_div(s->V, kSampleChunkLarge) >= 2 * kTargetBlocks ||
+                             s->V + 7 > kSampleMaxChunks * kSampleChunkSmall
+                         ? kSampleChunkLarge
+                         : kSampleChunkSmall;
+    // the smallest groups of which a row has few enough: top-k's bound, the
+    // k-th largest group maximum, needs many more groups than k
+    p->group_shift = s->V + 7 <= 4096 * 16 ? 4 : s->V + 7 <= kSampleMaxGroups * 64 ? 6 : 8;
     p->groups = ceil_div(s->V + 7, int64_t(1) << p->group_shift);
     p->chunks = ceil_div(s->V + 7, p->chunk_elems);
     const size_t n = static_cast<size_t>(s->N);

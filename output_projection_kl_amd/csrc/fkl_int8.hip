@@ -241,10 +241,13 @@ __global__ __launch_bounds__(256) void k_copy_rows(const int8_t* __restrict__ sr
     const int k0 = static_cast<int>(i - r * pieces) * 16;
     const int8_t* s = src + r * ld + k0;
     u32x4 v{0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (k0 + j < K)
+    if (k0 + 16 <= K) {
+      typedef u32x4 AnyPiece __attribute__((aligned(1)));
+      if (dcheck_range(dbg, 0, kDbgProjectOperand, s, 16)) v = *reinterpret_cast<const AnyPiece*>(s);
+    } else {
+      for (int j = 0; k0 + j < K; ++j)
         v[j / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(dload(dbg, 0, kDbgProjectOperand, s + j))) << (8 * (j % 4));
+    }
     dstore(dbg, 1, kDbgProjectWork, reinterpret_cast<u32x4*>(dst + i * 16), v);
   }
 }

@@ -13,7 +13,7 @@
 //
 // Three routes, by the row length:
 //   up to 1024 entries: k_sample_short, one wave per row, the row in registers.
-//   up to 2^18: k_sample_scan reads the logits once, spread over all CUs, and
+//   up to 2^20: k_sample_scan reads the logits once, spread over all CUs, and
 //     leaves per row the largest logit of every 64 entries and, where the
 //     filters need it, the mass or a mass histogram of every chunk;
 //     k_sample_pick, one workgroup per row, bounds the border from those,
@@ -495,7 +495,7 @@ __device__ __forceinline__ void sample_row_exact(const SampleParams& P, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Rows of up to 2^18 entries
+// Rows of up to 2^20 entries
 // ---------------------------------------------------------------------------
 
 template <class T>
@@ -586,7 +586,7 @@ struct RowView {
 // below it their weights in units of 2^-34 (16384 entries of at most 2^(1/16)
 // stay below 2^49). The rounding is 2^-35 of a weight either way: over n
 // entries the sums are off by sqrt(n) 2^-35 of a weight, and a draw differs
-// from that of exact sums with a probability below 1e-8 at 2^18 entries.
+// from that of exact sums with a probability below 1e-8.
 // Integer sums do not depend on their order.
 constexpr int kHistShift = 34;
 constexpr int kHistCount = 49;
@@ -653,6 +653,13 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
     if constexpr (kPer == 4) m = fmaxf(m, xor_lane_f32<8>(m));
     if (P.group_shift == 6 && e % 64 == 0 && e / 64 < P.groups)
       dstore(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + e / 64, logit_key(m));
+    if (P.group_shift == 8) {  // of 256: a wave's 64 pieces of 4, or half of its pieces of 8
+      if constexpr (kPer == 8) m = fmaxf(m, xor_lane_f32<8>(m));
+      m = fmaxf(m, xor_lane_f32<16>(m));
+      if constexpr (kPer == 4) m = fmaxf(m, xor_lane_f32<32>(m));
+      if (e % 256 == 0 && e / 256 < P.groups)
+        dstore(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + e / 256, logit_key(m));
+    }
     top = fmaxf(top, m);
   }
   if (mode == kMaximaOnly) return;
@@ -694,7 +701,7 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
     if (grid_fits(base, c8)) {
       const int first = static_cast<int>(base);
       // What lies below the last bin, 2^-64 of the chunk's largest weight, is
-      // left out: of 2^18 entries all together less than 2^-46 of the mass.
+      // left out: of 2^20 entries all together less than 2^-44 of the mass.
       // Masked entries and NaN are brought there.
       const float low = static_cast<float>((base - 2.0 * kScanBins) / c8);
 #pragma unroll
@@ -723,11 +730,11 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   }
 }
 
-constexpr int kMaxGroups = 4096;
+constexpr int kMaxGroups = kSampleMaxGroups;
 constexpr int kDistanceBins = 1024;  // of bound_of_kth
 constexpr int kFineBits = kRowThreads == 512 ? 9 : 10;
 static_assert(1 << kFineBits == kRowThreads, "one of border_entry's bins per thread");
-constexpr int kMaxChunks = 64;
+constexpr int kMaxChunks = kSampleMaxChunks;
 
 struct PickLds {
   union {

@@ -97,7 +97,7 @@ def test_workspace_sizes_hold_what_they_are_for():
     # nothing to hold: the workspace may be NULL
     if "debug" not in os.path.basename(fkl.library_path()):
         assert fkl.project_workspace_size(5, 1024, 1024) == 0 and fkl.sample_workspace_size(10, 1024) == 0
-    for N, V in ((3, 5000), (512, 201088), (64, 128256), (1, 262136)):
+    for N, V in ((3, 5000), (512, 201088), (64, 128256), (1, 262136), (2, 1048568)):
         assert 0 < fkl.sample_workspace_size(N, V) <= N * (V // 4096 + 2) * 5200 + 4096
 
 

@@ -186,9 +186,9 @@ def test_sample_strided_rows_ids_and_given_outputs(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("V", [262135, 262136, 262137, 300001])
+@pytest.mark.parametrize("V", [262135, 262136, 262137, 262144, 300001, 1048568, 1048569])
 def test_sample_the_longest_rows(V, dtype):
-    """Around the row length at which the route changes, from aligned and unaligned rows."""
+    """Around the row lengths at which the groups, chunks and the route change, from aligned and unaligned rows."""
     dev = _dev()
     wide, u = _logits(3, V + 8, V, dtype, dev)
     for lo in (0, 7):
