@@ -539,7 +539,7 @@ const char* fkl_last_error(void);
 
 /* Library version as MAJOR * 10000 + MINOR * 100 + PATCH (0.2.0: the plan
  * query, loss-term validation, the allocation-free forward and the fused
- * top-K builder). */
+ * top-K builder; 0.3.0: the 8-bit head and sampling). */
 int fkl_version(void);
 
 #ifdef __cplusplus

@@ -624,6 +624,6 @@ const char* fkl_status_string(fkl_status status) {
 
 const char* fkl_last_error(void) { return g_last_error.c_str(); }
 
-int fkl_version(void) { return 200; }
+int fkl_version(void) { return 300; }
 
 }  // extern "C"

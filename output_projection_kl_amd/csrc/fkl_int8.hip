@@ -136,7 +136,9 @@ __device__ __forceinline__ void pack_levels(const typename QuantOf<T>::Scale& s,
 
 // One workgroup per row, in pieces of 16 bytes of x; the row's last few
 // elements one by one. Pieces are read and written at any alignment (the GPU
-// splits an access that crosses a line).
+// splits an access that crosses a line). 128256 x 4096 bf16: 244 us, 6.45 TB/s
+// read and written (281 us without the non-temporal hint of ONCE); 4096 x 2880
+// bf16, which the caches hold: 10 us.
 template <class T, bool ONCE>
 __global__ __launch_bounds__(kQuantThreads) void k_quantize(const T* __restrict__ x, int64_t ldx, int cols,
                                                             int8_t* __restrict__ q, int64_t ldq,
@@ -231,7 +233,9 @@ hipError_t launch_quantize(int64_t rows, int64_t cols, int type, const void* x, 
 // ---------------------------------------------------------------------------
 
 // Rows of K bytes at any stride and alignment copied to rows of row16 bytes
-// (16-byte aligned, a multiple of 16); the bytes past K are zeroed.
+// (16-byte aligned, a multiple of 16); the bytes past K are zeroed. HBM bound:
+// 32003 x 2887 of stride 2889, 29 us, 6.4 TB/s read and written (92 us a byte at
+// a time).
 __global__ __launch_bounds__(256) void k_copy_rows(const int8_t* __restrict__ src, int64_t ld, int64_t rows, int K,
                                                    int row16, int8_t* __restrict__ dst, DebugCheck dbg) {
   const int pieces = row16 / 16;
@@ -621,8 +625,11 @@ __device__ __forceinline__ void int8_mainloop(const Operand& A, const Operand& B
   block_barrier();
 }
 
-// One output tile per workgroup. MFMA bound for the large tiles. The results
-// are staged in LDS in the output's type and stored as whole lines: stored
+// One output tile per workgroup. MFMA bound for the large tiles: 8192 x 128256 x
+// 4096 into bf16 takes 3.6 ms, 2390 TOP/s (5030 at the full rate; the GPU's clock
+// falls with the load). HBM bound for few rows: 1 x 201088 x 2880, 96 us, 6.0
+// TB/s; 48 x 128256 x 4096, 103 us, 5.2 TB/s, where the tiles' starts and ends
+// show. The results are staged in LDS in the output's type and stored as whole lines: stored
 // from the registers (32 bytes of a row at a time) they took a 8192 x 128256 x
 // 4096 product from 4.09 to 4.58 ms.
 template <class T, class C>
@@ -721,7 +728,8 @@ __global__ __launch_bounds__(C::kThreads) void k_project(ProjectParams P) {
   }
 }
 
-// The sums of a split contraction added up, scaled and rounded.
+// The sums of a split contraction added up, scaled and rounded. Launch bound:
+// the sums come from the cache (100 x 65 x 20011 in 14 us with the split product).
 template <class T>
 __global__ __launch_bounds__(256) void k_project_join(ProjectParams P, const int32_t* __restrict__ sums, int64_t ld) {
   const int64_t quads = (P.N + 3) / 4;

@@ -14,7 +14,7 @@
 // Three routes, by the row length:
 //   up to 1024 entries: k_sample_short, one wave per row, the row in registers.
 //   up to 2^20: k_sample_scan reads the logits once, spread over all CUs, and
-//     leaves per row the largest logit of every 64 entries and, where the
+//     leaves per row the largest logit of every 16, 64 or 256 entries and, where the
 //     filters need it, the mass or a mass histogram of every chunk;
 //     k_sample_pick, one workgroup per row, bounds the border from those,
 //     reads again only the groups that reach the bound (or one chunk), and
@@ -370,7 +370,10 @@ struct ExactLds {
 // One workgroup, any row: the border by radix selection over the row's
 // keys, eight bits at a time, first by count (top-k), then by mass (top-p),
 // and the draw by find_position. The masses of the selection are integers in
-// units of 2^-shift, whose sum does not depend on its order.
+// units of 2^-shift, whose sum does not depend on its order. Eight to ten reads
+// of the row by one CU, and LDS atomics: 0.75 ms for 128256 equal logits and
+// top-p, 0.9 to 1.3 ms for top-k 5000 with top-p, whatever the number of rows up
+// to one per CU.
 template <class T>
 __device__ __forceinline__ void sample_row_exact(const SampleParams& P, int64_t row, const RowSettings& S, uint32_t m_key,
                                               int shift, ExactLds& lds) {
@@ -610,8 +613,10 @@ __device__ __forceinline__ uint64_t hist_word(const EighthSeries& power, const E
 
 // One workgroup per chunk of a row. HBM bound where only the maxima are
 // wanted; with the masses, one fp64 exponential per entry (about 20 vector
-// instructions, and an LDS atomic for the histogram) takes longer than the
-// reading.
+// instructions, and an LDS atomic for the histogram) takes about as long as the
+// reading. 512 x 201088 fp32 with settings of every kind: 65 us, 6.3 TB/s; 64 x
+// 128256 bf16: 3 us for the maxima (5 TB/s, the launch's own time included), 11
+// us for the histograms.
 template <class T, int kThreads, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
   constexpr int kPer = RowView<T>::kPer;
@@ -942,7 +947,9 @@ __device__ __forceinline__ int settle_wave(const uint32_t (&key)[R], const RowSe
 }
 
 // Rows of up to 64 R entries, one wave each: latency of one row's chain of
-// steps for few rows, vector instructions (about 700 for R = 2) for many.
+// steps for few rows, vector instructions (about 700 for R = 2) for many. 64
+// rows of 100 fp32 logits: 3.5 us; 16384: 9 us, and 20 with top-p, whose border
+// takes a sort.
 template <class T, int R>
 __global__ __launch_bounds__(256) void k_sample_short(SampleParams P, int64_t rows) {
   const int lane = threadIdx.x & 63;
@@ -1682,7 +1689,11 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
 }
 
 // One workgroup per row, after k_sample_scan. Latency bound: a chain of short
-// steps over LDS, with one dependent read of the groups that reach the bound.
+// steps over LDS, with one dependent read of the groups that reach the bound (9
+// us for one row and top-k 50). Where top-p keeps thousands of entries, one CU's
+// vector instructions bound it: of the 27 us for a row of 128256 bf16 logits, 3.4
+// add up the histograms, 8 gather the border bin, 4 to 6 find the border in it,
+// 5 draw.
 // Up to one row per CU, a workgroup's waves have all of its registers (87);
 // with more rows two workgroups share it (64 registers, some spilled): 512 rows
 // of 201088 fp32 logits, 24 instead of 32 us; 64 rows of 128256 bf16 logits 32
@@ -1719,7 +1730,9 @@ __global__ __launch_bounds__(kRowThreads, WAVES) void k_sample_pick(SampleParams
   sample_row_exact<T>(P, row, S, m_key, shift, lds.exact);
 }
 
-// Rows longer than the scan takes: the largest key, then sample_row_exact.
+// Rows longer than the scan takes: the largest key, then sample_row_exact, all
+// of it by one CU per row (300001 fp32 logits: 0.35 ms without filters, 1.6 ms
+// with top-p).
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_sample_long(SampleParams P, int shift) {
   __shared__ ExactLds lds;
