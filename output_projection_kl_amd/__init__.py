@@ -16,6 +16,7 @@ and never stored, and backward forms them again.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -686,6 +687,22 @@ def _read_where_it_is(t, rows, cols, ld):
         t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16 <= t.untyped_storage().nbytes())
 
 
+@functools.lru_cache(maxsize=1024)
+def _project_shape(*fields):
+    """(reference to the shape, workspace bytes) of a product; the library only reads the shape."""
+    s, need = ctypes.byref(ProjectShape(*fields)), ctypes.c_size_t(0)
+    _check(lib().fkl_project_workspace_size(s, ctypes.byref(need)))
+    return s, need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _sample_shape(*fields):
+    """The same for sampling."""
+    s, need = ctypes.byref(SampleShape(*fields)), ctypes.c_size_t(0)
+    _check(lib().fkl_sample_workspace_size(s, ctypes.byref(need)))
+    return s, need.value
+
+
 def project_workspace_size(M, N, K, a_dtype=None, out_dtype=None, lda=None, ldb=None, ldo=None, flags=0) -> int:
     """Workspace bytes of project() for this shape (a_dtype int8 and contiguous rows unless given)."""
     torch = _torch()
@@ -735,12 +752,11 @@ def project(a, b, b_scale, a_scale=None, bias=None, out_dtype=None, out=None, wo
         flags |= PROJECT_COPY_A
     if not _read_where_it_is(b, N, K, ldb):
         flags |= PROJECT_COPY_B
-    s = ctypes.byref(ProjectShape(M, N, K, lda, ldb, ldo, code, _type_of(out, "out"), flags))
-    L, need = lib(), ctypes.c_size_t(0)
-    _check(L.fkl_project_workspace_size(s, ctypes.byref(need)))
-    ws = _workspace(need.value, dev, workspace) if need.value else None
-    _enqueue(dev, L.fkl_project, s, a.data_ptr(), None if a_scale is None else a_scale.data_ptr(), b.data_ptr(),
-             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(), need.value)
+    s, need = _project_shape(M, N, K, lda, ldb, ldo, code, _type_of(out, "out"), flags)
+    ws = _workspace(need, dev, workspace) if need else None
+    _enqueue(dev, lib().fkl_project, s, a.data_ptr(), None if a_scale is None else a_scale.data_ptr(), b.data_ptr(),
+             b_scale.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
+             None if ws is None else ws.data_ptr(), need)
     return out
 
 
@@ -792,13 +808,11 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, 
         logprob = torch.empty(N, dtype=f32, device=dev)
     else:
         _vector(logprob, "logprob", f32, N, dev)
-    s = ctypes.byref(SampleShape(N, V, ld, ld_ids, code))
+    s, need = _sample_shape(N, V, ld, ld_ids, code)
     params = SampleParams(T_rows, k_rows, p_rows, q_rows, T, max(-1, min(int(k), V)), p, q)
-    L, need = lib(), ctypes.c_size_t(0)
-    _check(L.fkl_sample_workspace_size(s, ctypes.byref(need)))
-    ws = _workspace(need.value, dev, workspace) if need.value else None
-    _enqueue(dev, L.fkl_sample, s, ctypes.byref(params), logits.data_ptr(), None if ids is None else ids.data_ptr(),
-             u.data_ptr(), token.data_ptr(), logprob.data_ptr(), None if ws is None else ws.data_ptr(), need.value)
+    ws = _workspace(need, dev, workspace) if need else None
+    _enqueue(dev, lib().fkl_sample, s, ctypes.byref(params), logits.data_ptr(), None if ids is None else ids.data_ptr(),
+             u.data_ptr(), token.data_ptr(), logprob.data_ptr(), None if ws is None else ws.data_ptr(), need)
     return token, logprob
 
 
