@@ -493,7 +493,7 @@ typedef struct {
 
 /* Workspace bytes of fkl_sample for this shape (host only; bytes may be
  * NULL): statistics of each row where V is above 1024, about 5 KiB for every
- * 4096 entries (16384 with many rows). 0 for shorter rows; the workspace may
+ * 4096 entries (8192 or 16384 of long rows). 0 for shorter rows; the workspace may
  * then be NULL. Errors: those of fkl_sample that the shape alone decides. */
 fkl_status fkl_sample_workspace_size(const fkl_sample_shape* shape, size_t* bytes);
 

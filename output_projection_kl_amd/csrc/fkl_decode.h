@@ -91,8 +91,7 @@ constexpr int64_t kSampleShortMaxV = 1024;
 constexpr int64_t kSampleScanMaxV = (int64_t(1) << 20) - 8;
 constexpr int64_t kSampleMaxGroups = 4160;  // a little over 2^18 / 64: rows of 2^18 entries at any alignment
 constexpr int64_t kSampleMaxChunks = 64;
-constexpr int64_t kSampleChunkSmall = 4096;   // elements per scan workgroup where there are few rows
-constexpr int64_t kSampleChunkLarge = 16384;
+constexpr int64_t kSampleChunk = 4096;  // elements per scan workgroup, or twice or four times as many
 constexpr int64_t kSampleHistBytes = 512 * 8;  // one chunk's mass histogram
 
 struct SampleArgs {

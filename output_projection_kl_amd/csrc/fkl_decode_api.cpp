@@ -221,11 +221,18 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   size_t off = kControlBytes;
   p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
   if (p->route == kSampleScan) {
-    // the larger chunks where they leave enough workgroups for every CU
-    p->chunk_elems = s->N * ceil_div(s->V, kSampleChunkLarge) >= 2 * kTargetBlocks ||
-                             s->V + 7 > kSampleMaxChunks * kSampleChunkSmall
-                         ? kSampleChunkLarge
-                         : kSampleChunkSmall;
+    // Chunks of 4096 entries, a workgroup of 256 threads each: the draw reads
+    // one, and small workgroups share the CUs evenly (130 x 50257 fp16 without
+    // filters: 12 us for the scan and 9 for the pick, 17 and 14 with chunks of
+    // 16384). Long rows add up their chunks' histograms: twice the chunk where
+    // that leaves two workgroups per CU (64 x 128256 bf16, top-p: 14.5 and 29.5
+    // us, 16 and 31 with 4096; 512 x 201088 fp32: 117 and 56, 122 and 67). The
+    // longest need the largest to have no more than 64.
+    p->chunk_elems = kSampleChunk;
+    if (s->V + 7 > kSampleMaxChunks * 2 * kSampleChunk) p->chunk_elems = 4 * kSampleChunk;
+    else if (s->V + 7 > kSampleMaxChunks * kSampleChunk ||
+             (s->V > 65536 && s->N * ceil_div(s->V, 2 * kSampleChunk) >= 2 * kTargetBlocks))
+      p->chunk_elems = 2 * kSampleChunk;
     // the smallest groups of which a row has few enough: top-k's bound, the
     // k-th largest group maximum, needs many more groups than k
     p->group_shift = s->V + 7 <= 4096 * 16 ? 4 : s->V + 7 <= kSampleMaxGroups * 64 ? 6 : 8;

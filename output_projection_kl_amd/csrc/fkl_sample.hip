@@ -614,7 +614,7 @@ __device__ __forceinline__ uint64_t hist_word(const EighthSeries& power, const E
 // One workgroup per chunk of a row. HBM bound where only the maxima are
 // wanted; with the masses, one fp64 exponential per entry (about 20 vector
 // instructions, and an LDS atomic for the histogram) takes about as long as the
-// reading. 512 x 201088 fp32 with settings of every kind: 65 us, 6.3 TB/s; 64 x
+// reading. 512 x 201088 fp32 with settings of every kind: 61 us, 6.7 TB/s; 64 x
 // 128256 bf16: 3 us for the maxima (5 TB/s, the launch's own time included), 11
 // us for the histograms.
 template <class T, int kThreads, bool ONCE>
@@ -1784,12 +1784,11 @@ static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hip
     {
       TraceScope ts(st, "sample_scan", 0.0, bytes);
       const dim3 grid(static_cast<unsigned>(rows * p.chunks));
-      if (p.chunk_elems == 256 * kScanElems)
-        hipLaunchKernelGGL((k_sample_scan<T, 256, false>), grid, dim3(256), 0, st, P);
-      else if (once)
-        hipLaunchKernelGGL((k_sample_scan<T, 1024, true>), grid, dim3(1024), 0, st, P);
-      else
-        hipLaunchKernelGGL((k_sample_scan<T, 1024, false>), grid, dim3(1024), 0, st, P);
+      const int threads = static_cast<int>(p.chunk_elems / kScanElems);
+      auto* const scan = threads == 256   ? once ? k_sample_scan<T, 256, true> : k_sample_scan<T, 256, false>
+                         : threads == 512 ? once ? k_sample_scan<T, 512, true> : k_sample_scan<T, 512, false>
+                                          : once ? k_sample_scan<T, 1024, true> : k_sample_scan<T, 1024, false>;
+      hipLaunchKernelGGL(scan, grid, dim3(static_cast<unsigned>(threads)), 0, st, P);
     }
     TraceScope ts(st, "sample_pick", 0.0, 4.0 * rows * p.groups);
     auto* const pick = rows > kTargetBlocks ? k_sample_pick<T, 8> : k_sample_pick<T, 4>;

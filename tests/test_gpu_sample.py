@@ -76,7 +76,7 @@ def test_sample_settings(V, dtype):
         _check(x, torch.roll(u, i), **s)
 
 
-@pytest.mark.parametrize("N,V", [(1, 201088), (300, 700), (64, 30000), (1025, 100), (260, 5000)])
+@pytest.mark.parametrize("N,V", [(1, 201088), (300, 700), (64, 30000), (1025, 100), (260, 5000), (70, 70001)])
 def test_sample_settings_for_each_row(N, V):
     dev = _dev()
     x, u = _logits(N, V, N + V, torch.float32, dev)
@@ -186,7 +186,7 @@ def test_sample_strided_rows_ids_and_given_outputs(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("V", [262135, 262136, 262137, 262144, 300001, 1048568, 1048569])
+@pytest.mark.parametrize("V", [262135, 262136, 262137, 262144, 300001, 524280, 524281, 1048568, 1048569])
 def test_sample_the_longest_rows(V, dtype):
     """Around the row lengths at which the groups, chunks and the route change, from aligned and unaligned rows."""
     dev = _dev()
@@ -269,7 +269,7 @@ def test_sample_wide_borders_of_either_sign(shift, N, dtype):
     _check(x, u, q=0.002)
 
 
-@pytest.mark.parametrize("dtype,N,V", [(torch.float32, 600, 120001), (torch.bfloat16, 1030, 150016)])
+@pytest.mark.parametrize("dtype,N,V", [(torch.float32, 600, 120001), (torch.bfloat16, 1030, 150016), (torch.float32, 1200, 60001)])
 def test_sample_logits_larger_than_the_cache(dtype, N, V):
     """Logits that are streamed past the last-level cache: the same draws as from their halves, which are not."""
     dev = _dev()
