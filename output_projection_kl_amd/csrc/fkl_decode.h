@@ -73,7 +73,7 @@ struct ProjectArgs {
   char* ws;
 };
 
-enum SampleRoute { kSampleShort, kSampleScan, kSampleLong };
+enum SampleRoute { kSampleShort, kSampleRow, kSampleScan, kSampleLong };
 
 struct SamplePlan {
   int64_t N, V, ld, ld_ids;
@@ -89,6 +89,7 @@ struct SamplePlan {
 
 constexpr int64_t kSampleShortMaxV = 1024;
 constexpr int64_t kSampleScanMaxV = (int64_t(1) << 20) - 8;
+constexpr int64_t kSampleRowMax = 8192;
 constexpr int64_t kSampleMaxGroups = 4160;  // a little over 2^18 / 64: rows of 2^18 entries at any alignment
 constexpr int64_t kSampleMaxChunks = 64;
 constexpr int64_t kSampleChunk = 4096;  // elements per scan workgroup, or twice or four times as many

@@ -216,11 +216,19 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
   if (s->ld > kMaxLd || s->ld_ids > kMaxLd) return set_error(FKL_EUNSUPPORTED, "ld and ld_ids must be <= 2^40");
   p->N = s->N, p->V = s->V, p->ld = s->ld, p->ld_ids = s->ld_ids;
   p->type = s->type;
-  p->route = s->V <= kSampleShortMaxV ? kSampleShort : s->V <= kSampleScanMaxV ? kSampleScan : kSampleLong;
+  // Short rows, up to one per CU, take one launch for the scan and the pick: a
+  // call of 64 x 8000 fp32 with top-k 50 and top-p, or with min-p, 11.3 instead
+  // of 13.4 us, most of either the host's. Longer rows lose more by a draw
+  // from the whole row than the launch costs (64 x 16000 without filters: 17
+  // instead of 14).
+  p->route = s->V <= kSampleShortMaxV                                                  ? kSampleShort
+             : s->V + 7 <= kSampleRowMax && s->N <= static_cast<int64_t>(kTargetBlocks) ? kSampleRow
+             : s->V <= kSampleScanMaxV                                                 ? kSampleScan
+                                                                                       : kSampleLong;
   p->groups = p->chunks = p->chunk_elems = p->group_shift = 0;
   size_t off = kControlBytes;
   p->off_group_max = p->off_chunk_max = p->off_chunk_mass = p->off_chunk_hist = off;
-  if (p->route == kSampleScan) {
+  if (p->route == kSampleRow || p->route == kSampleScan) {
     // Chunks of 4096 entries, a workgroup of 256 threads each: the draw reads
     // one, and small workgroups share the CUs evenly (130 x 50257 fp16 without
     // filters: 12 us for the scan and 9 for the pick, 17 and 14 with chunks of
@@ -229,7 +237,7 @@ fkl_status make_sample_plan(const fkl_sample_shape* s, SamplePlan* p) {
     // us, 16 and 31 with 4096; 512 x 201088 fp32: 117 and 56, 122 and 67). The
     // longest need the largest to have no more than 64.
     p->chunk_elems = kSampleChunk;
-    if (s->V + 7 > kSampleMaxChunks * 2 * kSampleChunk) p->chunk_elems = 4 * kSampleChunk;
+    if (p->route == kSampleRow || s->V + 7 > kSampleMaxChunks * 2 * kSampleChunk) p->chunk_elems = 4 * kSampleChunk;
     else if (s->V + 7 > kSampleMaxChunks * kSampleChunk ||
              (s->V > 65536 && s->N * ceil_div(s->V, 2 * kSampleChunk) >= 2 * kTargetBlocks))
       p->chunk_elems = 2 * kSampleChunk;

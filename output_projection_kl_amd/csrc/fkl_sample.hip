@@ -11,8 +11,10 @@
 // two orders of summation differ by less than 1e-15 of the total, far below
 // the smallest weight that is ever drawn in practice.
 //
-// Three routes, by the row length:
+// The routes, by the row length:
 //   up to 1024 entries: k_sample_short, one wave per row, the row in registers.
+//   up to 8192, for up to one row per CU: k_sample_row, the next route's two
+//     kernels in one.
 //   up to 2^20: k_sample_scan reads the logits once, spread over all CUs, and
 //     leaves per row the largest logit of every 16, 64 or 256 entries and, where the
 //     filters need it, the mass or a mass histogram of every chunk;
@@ -258,12 +260,14 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& P, int64
 }
 
 // What the scan leaves for a row beside the maxima: nothing where top-k or
-// min-p bound the border by themselves, each chunk's mass where the whole
+// min-p bound the border by themselves or a filtered row's entries can all be
+// held (64 x 2000 with top-k 50 and top-p: 10.5 us instead of 16 by histograms), each chunk's mass where the whole
 // row's mass counts, each chunk's mass histogram where top-p alone decides, or
 // top-k with too many entries for the group maxima to bound it well.
 enum RowMode { kMaximaOnly, kChunkMass, kMassHistogram };
 
 __device__ __forceinline__ RowMode row_mode(const RowSettings& s, const SampleParams& P) {
+  if (P.V <= kCandidates && (s.k < static_cast<uint32_t>(P.V) || s.p < 1.0)) return kMaximaOnly;  // all can be candidates
   if (s.k < static_cast<uint32_t>(P.V)) return s.k > static_cast<uint32_t>(P.groups) / 4 ? kMassHistogram : kMaximaOnly;
   if (s.p < 1.0) return s.q > 0.0 ? kChunkMass : kMassHistogram;
   return s.q > 0.0 ? kMaximaOnly : kChunkMass;
@@ -617,19 +621,25 @@ __device__ __forceinline__ uint64_t hist_word(const EighthSeries& power, const E
 // reading. 512 x 201088 fp32 with settings of every kind: 61 us, 6.7 TB/s; 64 x
 // 128256 bf16: 3 us for the maxima (5 TB/s, the launch's own time included), 11
 // us for the histograms.
+template <int kThreads>
+struct ScanLds {
+  uint64_t hist[kScanBins];
+  double eighth[8];
+  float wave_top[kThreads / 64];
+  double wave_mass[kThreads / 64];
+};
+
 template <class T, int kThreads, bool ONCE>
-__global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
+__device__ __forceinline__ void scan_chunk(const SampleParams& P, int64_t row, int chunk, ScanLds<kThreads>& L) {
   constexpr int kPer = RowView<T>::kPer;
   constexpr int kPieces = kScanElems / kPer;
   constexpr int kWaves = kThreads / 64;
-  __shared__ uint64_t hist[kScanBins];
-  __shared__ double eighth[8];
-  __shared__ float wave_top[kWaves];
-  __shared__ double wave_mass[kWaves];
+  uint64_t* const hist = L.hist;
+  double* const eighth = L.eighth;
+  float* const wave_top = L.wave_top;
+  double* const wave_mass = L.wave_mass;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int chunk = blockIdx.x % P.chunks;
-  const int64_t row = P.row0 + blockIdx.x / P.chunks;
   const RowView<T> view(P, row);
   const int64_t slot = row * P.chunks + chunk;
   u32x4 held[kPieces];
@@ -733,6 +743,12 @@ __global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
     dstore(P.dbg, 5, kDbgSampleWork, P.chunk_max + slot, logit_key(top));
     dstore(P.dbg, 5, kDbgSampleWork, P.chunk_mass + slot, s);
   }
+}
+
+template <class T, int kThreads, bool ONCE>
+__global__ __launch_bounds__(kThreads) void k_sample_scan(SampleParams P) {
+  __shared__ ScanLds<kThreads> lds;
+  scan_chunk<T, kThreads, ONCE>(P, P.row0 + blockIdx.x / P.chunks, blockIdx.x % P.chunks, lds);
 }
 
 constexpr int kMaxGroups = kSampleMaxGroups;
@@ -1051,16 +1067,17 @@ __device__ __forceinline__ void draw_in_chunk(const SampleParams& P, int64_t row
   constexpr int kPer = RowView<T>::kPer;
   const int tid = threadIdx.x;
   const int pieces = P.chunk_elems / kPer;
+  const int in_row = min(pieces, (view.lead + P.V + kPer - 1) / kPer - chunk * pieces);
   __syncthreads();
   if (tid == 0) L.word[0] = 0xffffffffu, L.word[1] = 0;
   int first_at = -1, last_at = -1;  // this thread's positions past the goal, and of positive weight
   double first_w = 0.0, last_w = 0.0;
-  for (int p0 = 0; p0 < pieces; p0 += kRowThreads) {
+  for (int p0 = 0; p0 < in_row; p0 += kRowThreads) {
     float x[kPer];
     double w[kPer], sum = 0.0, total;
     const int piece = chunk * pieces + p0 + tid;
     const int pos = piece * kPer - view.lead;
-    const bool live = p0 + tid < pieces;
+    const bool live = p0 + tid < in_row;
     if (live) view.logits(P.dbg, piece, x);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -1551,9 +1568,9 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   // a key that every kept entry reaches
   uint32_t bound = kMaskedKey + 1;
   if (!all && mode == kMaximaOnly) bound = S.k == 1 ? m_key : bound_of_kth(L, P.groups, m_key, S.k);
-  if (S.q > 0.0 && isfinite(m) && (S.p >= 1.0 || all)) {
+  if (S.q > 0.0 && isfinite(m) && (S.p >= 1.0 || whole >= 0.0)) {
     // w >= q: x >= m + log2(q) / c, taken lower by more than its rounding
-    // (top-p after top-k needs the mass of all the k entries: no bound from q then)
+    // (without the row's mass, top-p needs that of all the entries here: no bound from q then)
     const double lo = static_cast<double>(m) + log2(S.q) / S.c;
     const float low = static_cast<float>(lo - 1e-6 * fabs(lo) - 1e-30);
     bound = max(bound, logit_key(low));
@@ -1688,25 +1705,16 @@ __device__ __forceinline__ bool pick_row(const SampleParams& P, int64_t row, con
   return true;
 }
 
-// One workgroup per row, after k_sample_scan. Latency bound: a chain of short
-// steps over LDS, with one dependent read of the groups that reach the bound (9
-// us for one row and top-k 50). Where top-p keeps thousands of entries, one CU's
-// vector instructions bound it: of the 27 us for a row of 128256 bf16 logits, 3.4
-// add up the histograms, 8 gather the border bin, 4 to 6 find the border in it,
-// 5 draw.
-// Up to one row per CU, a workgroup's waves have all of its registers (87);
-// with more rows two workgroups share it (64 registers, some spilled): 512 rows
-// of 201088 fp32 logits, 24 instead of 32 us; 64 rows of 128256 bf16 logits 32
-// instead of 30 us.
-template <class T, int WAVES>
-__global__ __launch_bounds__(kRowThreads, WAVES) void k_sample_pick(SampleParams P, int shift) {
-  __shared__ union {
-    PickLds pick;
-    ExactLds exact;
-  } lds;
+union RowLds {
+  ScanLds<kRowThreads> scan;
+  PickLds pick;
+  ExactLds exact;
+};
+
+template <class T>
+__device__ __forceinline__ void pick_or_exact(const SampleParams& P, int64_t row, int shift, RowLds& lds) {
   PickLds& L = lds.pick;
   const int tid = threadIdx.x;
-  const int64_t row = P.row0 + blockIdx.x;
   uint32_t m_key = 0;
   for (int g = tid; g < P.groups; g += kRowThreads) {
     const uint32_t v = dload(P.dbg, 5, kDbgSampleWork, P.group_max + row * P.groups + g);
@@ -1728,6 +1736,33 @@ __global__ __launch_bounds__(kRowThreads, WAVES) void k_sample_pick(SampleParams
   if (pick_row<T>(P, row, S, view, m_key, L)) return;
   __syncthreads();
   sample_row_exact<T>(P, row, S, m_key, shift, lds.exact);
+}
+
+// One workgroup per row, after k_sample_scan. Latency bound: a chain of short
+// steps over LDS, with one dependent read of the groups that reach the bound (9
+// us for one row and top-k 50). Where top-p keeps thousands of entries, one CU's
+// vector instructions bound it: of the 27 us for a row of 128256 bf16 logits, 3.4
+// add up the histograms, 8 gather the border bin, 4 to 6 find the border in it,
+// 5 draw.
+// Up to one row per CU, a workgroup's waves have all of its registers (87);
+// with more rows two workgroups share it (64 registers, some spilled): 512 rows
+// of 201088 fp32 logits, 24 instead of 32 us; 64 rows of 128256 bf16 logits 32
+// instead of 30 us.
+template <class T, int WAVES>
+__global__ __launch_bounds__(kRowThreads, WAVES) void k_sample_pick(SampleParams P, int shift) {
+  __shared__ RowLds lds;
+  pick_or_exact<T>(P, P.row0 + blockIdx.x, shift, lds);
+}
+
+// Scan and pick of a row of one chunk, up to one row per CU: what the scan
+// leaves is read by the workgroup that wrote it. Launch bound.
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_sample_row(SampleParams P, int shift) {
+  __shared__ RowLds lds;
+  const int64_t row = P.row0 + blockIdx.x;
+  scan_chunk<T, kRowThreads, false>(P, row, 0, lds.scan);
+  __syncthreads();
+  pick_or_exact<T>(P, row, shift, lds);
 }
 
 // Rows longer than the scan takes: the largest key, then sample_row_exact, all
@@ -1774,6 +1809,11 @@ static void launch_sample_of(const SamplePlan& p, SampleParams P, int shift, hip
                             : k_sample_short<T, 16>;
       TraceScope ts(st, "sample_short", 0.0, bytes);
       hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), 0, st, P, rows);
+      continue;
+    }
+    if (p.route == kSampleRow) {
+      TraceScope ts(st, "sample_row", 0.0, bytes);
+      hipLaunchKernelGGL(k_sample_row<T>, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st, P, shift);
       continue;
     }
     if (p.route == kSampleLong) {

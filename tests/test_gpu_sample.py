@@ -12,7 +12,7 @@ from oracle import decode_oracle as oracle
 pytestmark = pytest.mark.gpu
 
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
-SIZES = [1, 2, 7, 63, 64, 65, 100, 255, 1000, 1024, 1025, 2048, 4097, 8191, 20000, 50257, 131075]
+SIZES = [1, 2, 7, 63, 64, 65, 100, 255, 1000, 1024, 1025, 2048, 4097, 8185, 8186, 8191, 20000, 50257, 131075]
 
 
 def _dev():
