@@ -261,9 +261,10 @@ __device__ __forceinline__ RowSettings row_settings(const SampleParams& P, int64
 
 // What the scan leaves for a row beside the maxima: nothing where top-k or
 // min-p bound the border by themselves or a filtered row's entries can all be
-// held (64 x 2000 with top-k 50 and top-p: 10.5 us instead of 16 by histograms), each chunk's mass where the whole
-// row's mass counts, each chunk's mass histogram where top-p alone decides, or
-// top-k with too many entries for the group maxima to bound it well.
+// held (64 x 2000 with top-k 50 and top-p: 10.5 us instead of 16 by
+// histograms), each chunk's mass where the whole row's mass counts, each chunk's
+// mass histogram where top-p alone decides, or top-k with too many entries for
+// the group maxima to bound it well.
 enum RowMode { kMaximaOnly, kChunkMass, kMassHistogram };
 
 __device__ __forceinline__ RowMode row_mode(const RowSettings& s, const SampleParams& P) {
